@@ -71,6 +71,7 @@ extern "C" {
 #define LA_BF16              0  /* bf16 GEMM operands and attention operands, fp32
                                    accumulation, fp32 residual stream and latent x    */
 #define LA_FP32              1  /* fp32 everywhere (SIMT path, no TF32)                */
+#define LA_FP16              2  /* op-level rotary and 8-bit cache entry points only   */
 #define LA_CACHE_TIMESTEP    0  /* each step keeps the noisy K/V it computed in its own
                                    cache (timestep forcing; papernotes note, key design
                                    4; gitcode blog, question 6)                         */
@@ -556,6 +557,113 @@ int la_op_attention_fp8(const void* q_codes, int64_t Tq, int32_t H, int32_t d, i
 int la_op_attention_static(const void* q, int64_t Tq, int32_t H, int32_t d, int32_t nseg,
                            const void* const* k_seg, const void* const* v_seg,
                            const int64_t* seg_len, void* out, float* out32, void* cuda_stream);
+
+/*
+ * Rotary positions with one to LA_MAX_AXES axes (time, height, width), given by
+ * a position for every token and axis instead of the stream's fixed grid.  No
+ * counterpart on the pages.
+ *   pos DEVICE int32 [tokens, naxes]; pairs HOST int32 [naxes], sum n >= 1 and
+ *   2 n <= head_dim; the first pairs[0] pairs turn with axis 0, the next
+ *   pairs[1] with axis 1, and so on: pair j of an axis by
+ *   a = pos * theta^(-j / pairs[axis]) (the stream's frequencies), theta >= 1.
+ *   half 0: pair i of a row is elements (2i, 2i+1); 1: (i, i + n).
+ *   out = (x0 cos a - x1 sin a, x0 sin a + x1 cos a), elements 2n.. unchanged;
+ *   inverse != 0 turns by -a, which undoes the rotation and is its gradient.
+ * Angles are exact modulo one turn for every int32 position.  x, out: DEVICE
+ * [tokens, heads, head_dim] of dtype (LA_BF16, LA_FP16 or LA_FP32; fp32 inside,
+ * rounded once), element strides of tokens and heads given, head_dim contiguous
+ * and at most 256.  out == x with the same strides works in place; otherwise the
+ * two must not overlap.  tokens == 0 does nothing.
+ */
+#define LA_MAX_AXES 4
+int la_op_rope_axes(int32_t dtype, const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                    void* out, int64_t out_token_stride, int64_t out_head_stride, int64_t tokens,
+                    int32_t heads, int32_t head_dim, const int32_t* pos, int32_t naxes,
+                    const int32_t* pairs, double theta, int32_t half, int32_t inverse,
+                    void* cuda_stream);
+
+/*
+ * A cache of keys and values in pages of e4m3 codes, one fp32 scale for each
+ * (page, head): value = code * scale.  No counterpart on the pages.  Key j of
+ * sequence b lies in page block_table[b, j / page_tokens], row j % page_tokens.
+ * All pointers are DEVICE; sizes are those of the arrays.
+ */
+typedef struct la_paged_cache {
+  void* k_pages;               /* uint8 [num_pages, heads, page_tokens, head_dim], 16-byte aligned */
+  void* v_pages;
+  float* k_scale;              /* fp32 [num_pages, heads], positive (NaN: see the append) */
+  float* v_scale;
+  const int32_t* block_table;  /* int32 [batch, max_pages] */
+  int32_t num_pages;
+  int32_t heads;               /* key / value heads */
+  int32_t page_tokens;         /* 32, 64 or 128 */
+  int32_t head_dim;            /* 64 or 128 */
+  int32_t batch;               /* sequences, 1..65535 */
+  int32_t max_pages;           /* columns of block_table */
+} la_paged_cache;
+
+/*
+ * Appends keys, rotated as la_op_rope_axes (naxes 0: not rotated), and values
+ * to the cache.  k, v: DEVICE [tokens, cache heads, head_dim] of dtype, strides
+ * as above.  Rows cu_new[b] .. cu_new[b+1]-1 (DEVICE int32 [batch + 1],
+ * ascending, at most max_new of them) become keys cache_len[b] .. of sequence b
+ * (DEVICE int32 [batch]); rows behind cu_new[batch] are not read.  cache_len is
+ * not written: the caller counts.
+ *   The scale of a page that gets new tokens is 2^e, the smallest with
+ *   448 * 2^e >= the largest magnitude among them (e >= -64), or the page's old
+ *   scale where that is larger and the page already holds tokens of the
+ *   sequence (cache_len[b] is not a multiple of page_tokens).  code = e4m3(value
+ *   / scale), to nearest even; where the scale grows, older codes of the page
+ *   become e4m3(code * old / new).  Rows of the page behind the last new token
+ *   keep their codes.  A new value that is not finite makes the scale NaN (codes
+ *   0), and it stays NaN until the page's first token is written again.
+ * A page may receive tokens of one sequence only in a call, and a page that
+ * several sequences read must not be appended to (copy it first): the library
+ * does not check this.  A sequence whose cu_new, cache_len or block_table
+ * entries do not fit the arrays is left out (a bad page alone is), and the
+ * op-level error word reports it (la_op_status: LA_EDEVICE).
+ */
+int la_op_cache_append_fp8(const la_paged_cache* cache, int32_t dtype, const void* k,
+                           int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                           int64_t v_token_stride, int64_t v_head_stride, int64_t tokens,
+                           const int32_t* cu_new, const int32_t* cache_len, int64_t max_new,
+                           const int32_t* pos, int32_t naxes, const int32_t* pairs, double theta,
+                           int32_t half, void* cuda_stream);
+
+/*
+ * Attention of a ragged batch of queries over the cache.  q, out: DEVICE
+ * [tokens, heads, head_dim] of dtype (LA_BF16 or LA_FP16), strides as above (out
+ * 8-byte aligned, its strides multiples of 4 elements); heads is a multiple of
+ * the cache's, head h reads key head h / (heads / cache heads).  Sequence b has
+ * the n = cu_q[b+1] - cu_q[b] <= max_q rows from cu_q[b] (DEVICE int32 [batch +
+ * 1], ascending) and L = kv_len[b] keys (DEVICE int32 [batch]; for queries whose
+ * own keys were appended, the length after the append).
+ *   o[r] = sum_j softmax_j(scale * q[r] . k[j]) v[j] over the keys that row r
+ *   sees: j < L and, with causal_block c > 0, j < (L - n) + (r / c + 1) * c: the
+ *   rows are the sequence's last n tokens in blocks of c that see themselves and
+ *   all before (1: token-causal; frames or latent blocks for more).
+ * A row that sees no key is 0.  Rows of no sequence are not written.  Inside: q
+ * in fp16 under a power of two per row, codes exactly, P in fp16 (unrounded in
+ * the normaliser), sums in fp32, one rounding to dtype.  out32, if not NULL:
+ * DEVICE fp32 [tokens, heads, head_dim] dense, 16-byte aligned, the value before
+ * that rounding.  A page whose scale is NaN makes the rows that see any key of
+ * it NaN.
+ * max_kv, a bound of kv_len, steers the split of the keys only.  workspace:
+ * DEVICE, 16-byte aligned, at least la_op_attention_cache_fp8_workspace bytes for
+ * the same arguments (0: may be NULL); calls that may run at the same time need
+ * one each.  Results do not depend on what it holds.  A sequence or page that
+ * does not fit the arrays is reported as by the append (its rows are not
+ * written; keys of a bad page count as zero keys and values).
+ */
+int64_t la_op_attention_cache_fp8_workspace(const la_paged_cache* cache, int64_t tokens,
+                                            int32_t heads, int64_t max_q, int64_t max_kv);
+int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const void* q,
+                              int64_t q_token_stride, int64_t q_head_stride, int64_t tokens,
+                              int32_t heads, const int32_t* cu_q, const int32_t* kv_len,
+                              int64_t max_q, int64_t max_kv, int32_t causal_block, double scale,
+                              void* out, int64_t out_token_stride, int64_t out_head_stride,
+                              float* out32, void* workspace, int64_t workspace_bytes,
+                              void* cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,7 @@ LIB_PATH = os.path.join(_HERE, "libla.so")
 LA_OK, LA_EINVAL, LA_ESTATE, LA_ENOMEM, LA_ECUDA, LA_EDEVICE = 0, -1, -2, -3, -4, -5
 LA_SINK_FIXED, LA_SINK_AAS = 0, 1
 LA_SCHED_PIPELINED, LA_SCHED_SEQUENTIAL = 0, 1
-LA_BF16, LA_FP32 = 0, 1
+LA_BF16, LA_FP32, LA_FP16 = 0, 1, 2
 LA_MAX_STEPS, LA_MAX_WINDOW, LA_MAX_FPB = 8, 14, 7
 LA_EPI_STORE, LA_EPI_RESID, LA_EPI_SET32, LA_EPI_EULER, LA_EPI_STORE32 = 0, 1, 2, 3, 4
 
@@ -39,6 +39,12 @@ class LaWeights(ctypes.Structure):
                 ("w_out", POINTER(c_void_p)), ("w_ffn1", POINTER(c_void_p)), ("w_ffn2", POINTER(c_void_p)),
                 ("ada", c_void_p), ("w_qc", POINTER(c_void_p)), ("w_kvc", POINTER(c_void_p)),
                 ("w_oc", POINTER(c_void_p))]
+
+
+class LaPagedCache(ctypes.Structure):
+    _fields_ = [("k_pages", c_void_p), ("v_pages", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("block_table", c_void_p), ("num_pages", c_int32), ("heads", c_int32), ("page_tokens", c_int32),
+                ("head_dim", c_int32), ("batch", c_int32), ("max_pages", c_int32)]
 
 
 class LaError(RuntimeError):
@@ -95,6 +101,15 @@ def load():
         "la_op_attention_fp8": (c_int, [c_void_p, c_int64, c_int32, c_int32, c_int32, POINTER(c_void_p),
                                         POINTER(c_void_p), POINTER(c_int64), c_void_p, c_void_p, c_void_p,
                                         c_void_p, c_void_p, c_void_p]),
+        "la_op_rope_axes": (c_int, [c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int64, c_int32,
+                                    c_int32, c_void_p, c_int32, c_void_p, c_double, c_int32, c_int32, c_void_p]),
+        "la_op_cache_append_fp8": (c_int, [c_void_p, c_int32, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64,
+                                           c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_void_p,
+                                           c_double, c_int32, c_void_p]),
+        "la_op_attention_cache_fp8_workspace": (c_int64, [c_void_p, c_int64, c_int32, c_int64, c_int64]),
+        "la_op_attention_cache_fp8": (c_int, [c_void_p, c_int32, c_void_p, c_int64, c_int64, c_int64, c_int32,
+                                              c_void_p, c_void_p, c_int64, c_int64, c_int32, c_double, c_void_p,
+                                              c_int64, c_int64, c_void_p, c_void_p, c_int64, c_void_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -115,6 +130,8 @@ def exported_symbols():
         "la_launch_count", "la_op_gemm", "la_op_attention", "la_op_euler", "la_op_attention_static",
         "la_debug_wait_timeout", "la_op_quantize_e4m3", "la_op_gemm_fp8", "la_op_attention_fp8",
         "la_debug_op_wait_timeout", "la_op_status", "la_sched_state_size", "la_sched_trace",
+        "la_op_rope_axes", "la_op_cache_append_fp8", "la_op_attention_cache_fp8",
+        "la_op_attention_cache_fp8_workspace",
     ]
 
 

@@ -132,3 +132,53 @@ struct ModArgs {
 // out = rms-normalised h * (1 + scale[row / rows_per_group]) + shift[...], bf16 and / or fp32.
 cudaError_t launch_rmsnorm_mod(const float* h, long long rows, long long D, float eps, const ModArgs& m,
                                void* out_bf16, float* out_f32, cudaStream_t st);
+
+// ---- rotary positions and the paged 8-bit cache ------------------------------------------
+// Rotated pairs and their angles a position step (see rotary.cuh).
+#define LA_ROPE_MAX_PAIRS 128
+struct RotaryTable {
+  unsigned long long turn[LA_ROPE_MAX_PAIRS];   // omega_j / (2 pi) in units of 2^-64 turns
+  unsigned char axis[LA_ROPE_MAX_PAIRS];
+  int n;                                        // rotated pairs; elements 2n.. pass through
+  int naxes;                                    // int32 positions a token
+  int half;                                     // 0: pair j = (2j, 2j+1); 1: (j, j + n)
+  int inverse;
+};
+struct RopeAxesParams {
+  const void* x; void* out;            // [tokens, heads, d], strides in elements, d contiguous
+  const int* pos;                      // [tokens, naxes]
+  long long tokens, x_st, x_sh, o_st, o_sh;
+  int heads, d;
+  int units, heads_per_thread;         // set by the launcher
+};
+cudaError_t launch_rope_axes(int dtype, const RopeAxesParams& p, const RotaryTable& tab, int num_sms, cudaStream_t st);
+
+struct CacheAppendParams {
+  const void* k; const void* v;        // [tokens, heads, d], strides in elements
+  long long k_st, k_sh, v_st, v_sh;
+  const int* pos;                      // [tokens, naxes] (tab.n > 0)
+  uint8_t* k_pages; uint8_t* v_pages;  // [num_pages, heads, page_tokens, d]
+  float* k_scale; float* v_scale;      // [num_pages, heads]
+  const int* block_table;              // [batch, max_pages]
+  const int* cache_len;                // [batch] tokens before the append
+  const int* cu_new;                   // [batch + 1] rows of each sequence in k and v
+  int tokens, batch, heads, d, page_tokens, num_pages, max_pages, max_new;
+  int pages_per_seq, heads_per_cta;    // set by the launcher
+  int* err;
+};
+cudaError_t launch_cache_append(int dtype, const CacheAppendParams& p, const RotaryTable& tab, int num_sms, cudaStream_t st);
+
+struct AttnCacheParams {
+  const void* q;                       // [tokens, heads, d], strides in elements
+  void* out; float* out32;             // out with strides; out32 optional, dense
+  long long q_st, q_sh, o_st, o_sh;
+  const uint8_t* k_pages; const uint8_t* v_pages;
+  const float* k_scale; const float* v_scale;
+  const int* block_table; const int* kv_len; const int* cu_q;
+  int tokens, batch, heads, kv_heads, d, page_tokens, num_pages, max_pages, max_q, causal_block;
+  float scale_log2;                    // softmax scale * log2(e)
+  int nsplit;                          // pieces of the key axis
+  float* part_o; float2* part_ml;      // nsplit > 1: [nsplit, tokens, heads, d], [nsplit, tokens, heads]
+  int* err;
+};
+cudaError_t launch_attn_cache(int dtype, const AttnCacheParams& p, cudaStream_t st);

@@ -1,0 +1,207 @@
+// Op-level C entry points for rotary positions with several axes and the paged
+// 8-bit cache: argument checks, the frequency table, the split of the key axis.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kernels.h"
+#include "la_stream.h"
+
+namespace {
+
+int num_sms_current() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+int ret(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ECUDA; }
+
+constexpr int64_t kMaxRows = 1LL << 30;
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+size_t elem_size(int32_t dtype) { return dtype == LA_FP32 ? 4 : 2; }
+bool known_dtype(int32_t dtype) { return dtype == LA_BF16 || dtype == LA_FP32 || dtype == LA_FP16; }
+
+// omega_{a,j} = theta^(-j / pairs[a]), as a fraction of a turn in units of 2^-64.
+// long double keeps all 64 bits that the product with a position uses.
+bool fill_table(RotaryTable& t, int32_t d, int32_t naxes, const int32_t* pairs, double theta, int32_t half,
+                int32_t inverse) {
+  t.n = 0;
+  t.naxes = naxes;
+  t.half = half != 0;
+  t.inverse = inverse != 0;
+  if (naxes < 0 || naxes > LA_MAX_AXES || (naxes > 0 && !pairs)) return false;
+  if (naxes > 0 && !(theta >= 1.0 && theta <= 1e12)) return false;
+  constexpr long double two_pi = 6.283185307179586476925286766559005768L;
+  for (int a = 0; a < naxes; ++a) {
+    if (pairs[a] < 0 || pairs[a] > d / 2 - t.n) return false;
+    for (int j = 0; j < pairs[a]; ++j) {
+      const long double turns = powl(theta, -static_cast<long double>(j) / pairs[a]) / two_pi;   // <= 1 / (2 pi)
+      t.turn[t.n] = static_cast<unsigned long long>(roundl(ldexpl(turns, 64)));
+      t.axis[t.n++] = static_cast<unsigned char>(a);
+    }
+  }
+  return naxes == 0 || t.n > 0;
+}
+
+bool strides_fit(int64_t rows, int64_t st, int64_t sh, int32_t heads, int32_t d) {
+  return st >= 0 && sh >= 0 && (heads == 1 || sh >= d) && (rows <= 1 || st >= 1) && st <= (1LL << 40) && sh <= (1LL << 40);
+}
+
+bool cache_fine(const la_paged_cache* c) {
+  if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->block_table) return false;
+  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return false;
+  if (c->head_dim != 64 && c->head_dim != 128) return false;
+  if (c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128) return false;
+  return c->num_pages >= 1 && c->heads >= 1 && c->heads <= 65535 && c->batch >= 1 && c->batch <= 65535 && c->max_pages >= 1 &&
+         static_cast<int64_t>(c->max_pages) * c->page_tokens <= kMaxRows;
+}
+
+// Pieces of the key axis: enough CTAs (16 rows each) for 3 on every SM, each with
+// at least 256 keys.
+int plan_split(int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
+  const int64_t rows = max_q * (heads / kv_heads);
+  const int64_t ctas = (rows + 15) / 16 * kv_heads * batch;
+  const int64_t want = 148 * 3;
+  return static_cast<int>(std::max<int64_t>(1, std::min((want + ctas - 1) / std::max<int64_t>(ctas, 1), max_kv / 256)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int la_op_rope_axes(int32_t dtype, const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                    int64_t out_token_stride, int64_t out_head_stride, int64_t tokens, int32_t heads, int32_t head_dim,
+                    const int32_t* pos, int32_t naxes, const int32_t* pairs, double theta, int32_t half, int32_t inverse,
+                    void* cuda_stream) {
+  if (!known_dtype(dtype) || tokens < 0 || tokens > kMaxRows || heads < 1 || heads > 65535) return LA_EINVAL;
+  if (head_dim < 2 || head_dim > 2 * LA_ROPE_MAX_PAIRS || naxes < 1) return LA_EINVAL;
+  if (!strides_fit(tokens, x_token_stride, x_head_stride, heads, head_dim) ||
+      !strides_fit(tokens, out_token_stride, out_head_stride, heads, head_dim))
+    return LA_EINVAL;
+  RotaryTable tab;
+  if (!fill_table(tab, head_dim, naxes, pairs, theta, half, inverse)) return LA_EINVAL;
+  if (tokens == 0) return LA_OK;
+  if (!x || !out || !pos || !aligned(x, elem_size(dtype)) || !aligned(out, elem_size(dtype)) || !aligned(pos, 4)) return LA_EINVAL;
+  RopeAxesParams p{};
+  p.x = x;
+  p.out = out;
+  p.pos = pos;
+  p.tokens = tokens;
+  p.x_st = x_token_stride;
+  p.x_sh = x_head_stride;
+  p.o_st = out_token_stride;
+  p.o_sh = out_head_stride;
+  p.heads = heads;
+  p.d = head_dim;
+  return ret(launch_rope_axes(dtype, p, tab, num_sms_current(), static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int la_op_cache_append_fp8(const la_paged_cache* cache, int32_t dtype, const void* k, int64_t k_token_stride,
+                           int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                           int64_t tokens, const int32_t* cu_new, const int32_t* cache_len, int64_t max_new,
+                           const int32_t* pos, int32_t naxes, const int32_t* pairs, double theta, int32_t half,
+                           void* cuda_stream) {
+  if (!cache_fine(cache) || !known_dtype(dtype) || tokens < 0 || tokens > kMaxRows || max_new < 0 || max_new > kMaxRows)
+    return LA_EINVAL;
+  if (!strides_fit(tokens, k_token_stride, k_head_stride, cache->heads, cache->head_dim) ||
+      !strides_fit(tokens, v_token_stride, v_head_stride, cache->heads, cache->head_dim))
+    return LA_EINVAL;
+  RotaryTable tab;
+  if (!fill_table(tab, cache->head_dim, naxes, pairs, theta, half, 0)) return LA_EINVAL;
+  if (!cu_new || !cache_len || (tab.n > 0 && tokens > 0 && !pos)) return LA_EINVAL;
+  if (tokens == 0 || max_new == 0) return LA_OK;
+  if (!k || !v || !aligned(k, elem_size(dtype)) || !aligned(v, elem_size(dtype))) return LA_EINVAL;
+  CacheAppendParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_st = k_token_stride;
+  p.k_sh = k_head_stride;
+  p.v_st = v_token_stride;
+  p.v_sh = v_head_stride;
+  p.pos = pos;
+  p.k_pages = static_cast<uint8_t*>(cache->k_pages);
+  p.v_pages = static_cast<uint8_t*>(cache->v_pages);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.block_table = cache->block_table;
+  p.cache_len = cache_len;
+  p.cu_new = cu_new;
+  p.tokens = static_cast<int>(tokens);
+  p.batch = cache->batch;
+  p.heads = cache->heads;
+  p.d = cache->head_dim;
+  p.page_tokens = cache->page_tokens;
+  p.num_pages = cache->num_pages;
+  p.max_pages = cache->max_pages;
+  p.max_new = static_cast<int>(std::min(max_new, tokens));
+  if (op_error_word(&p.err) != LA_OK) return LA_ECUDA;
+  return ret(launch_cache_append(dtype, p, tab, num_sms_current(), static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int64_t la_op_attention_cache_fp8_workspace(const la_paged_cache* cache, int64_t tokens, int32_t heads, int64_t max_q,
+                                            int64_t max_kv) {
+  if (!cache_fine(cache) || heads < 1 || heads % cache->heads != 0 || tokens < 0 || tokens > kMaxRows || max_q < 0 ||
+      max_q > kMaxRows || max_kv < 0 || max_kv > kMaxRows)
+    return LA_EINVAL;
+  const int n = plan_split(std::min(max_q, tokens), max_kv, cache->batch, heads, cache->heads);
+  return n == 1 ? 0 : n * tokens * heads * (cache->head_dim * 4LL + 8);
+}
+
+int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const void* q, int64_t q_token_stride,
+                              int64_t q_head_stride, int64_t tokens, int32_t heads, const int32_t* cu_q,
+                              const int32_t* kv_len, int64_t max_q, int64_t max_kv, int32_t causal_block, double scale,
+                              void* out, int64_t out_token_stride, int64_t out_head_stride, float* out32, void* workspace,
+                              int64_t workspace_bytes, void* cuda_stream) {
+  if (!cache_fine(cache) || (dtype != LA_BF16 && dtype != LA_FP16)) return LA_EINVAL;
+  if (heads < 1 || heads % cache->heads != 0 || tokens < 0 || tokens > kMaxRows || max_q < 0 || max_q > kMaxRows ||
+      max_kv < 0 || max_kv > kMaxRows || causal_block < 0 || !(scale > 0.0 && scale < 1e30))
+    return LA_EINVAL;
+  if (!strides_fit(tokens, q_token_stride, q_head_stride, heads, cache->head_dim) ||
+      !strides_fit(tokens, out_token_stride, out_head_stride, heads, cache->head_dim))
+    return LA_EINVAL;
+  if (!cu_q || !kv_len) return LA_EINVAL;
+  const int64_t need = la_op_attention_cache_fp8_workspace(cache, tokens, heads, max_q, max_kv);
+  if (need < 0 || workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 16)))) return LA_EINVAL;
+  if (tokens == 0 || max_q == 0) return LA_OK;
+  if (!q || !out || !aligned(q, 2) || !aligned(out, 8) || out_token_stride % 4 != 0 || out_head_stride % 4 != 0 ||
+      !aligned(out32, 16))
+    return LA_EINVAL;
+  AttnCacheParams p{};
+  p.q = q;
+  p.out = out;
+  p.out32 = out32;
+  p.q_st = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.o_st = out_token_stride;
+  p.o_sh = out_head_stride;
+  p.k_pages = static_cast<const uint8_t*>(cache->k_pages);
+  p.v_pages = static_cast<const uint8_t*>(cache->v_pages);
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.block_table = cache->block_table;
+  p.kv_len = kv_len;
+  p.cu_q = cu_q;
+  p.tokens = static_cast<int>(tokens);
+  p.batch = cache->batch;
+  p.heads = heads;
+  p.kv_heads = cache->heads;
+  p.d = cache->head_dim;
+  p.page_tokens = cache->page_tokens;
+  p.num_pages = cache->num_pages;
+  p.max_pages = cache->max_pages;
+  p.max_q = static_cast<int>(std::min(max_q, tokens));
+  p.causal_block = causal_block;
+  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  p.nsplit = plan_split(p.max_q, max_kv, p.batch, heads, cache->heads);
+  if (p.nsplit > 1) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + p.nsplit * tokens * heads * p.d);
+  }
+  if (op_error_word(&p.err) != LA_OK) return LA_ECUDA;
+  return ret(launch_attn_cache(dtype, p, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+}  // extern "C"

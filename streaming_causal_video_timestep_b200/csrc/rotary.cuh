@@ -1,0 +1,87 @@
+// Rotary positions with several axes, shared by k_rope_axes and the cache append.
+//
+// Pair j (of n) turns by pos[axis(j)] * omega_j.  The angle is kept in turns as a
+// 64-bit fixed-point fraction: omega_j / (2 pi) * 2^64 is rounded once on the host
+// and the product with the (signed) position wraps modulo 2^64, which is exactly
+// "modulo one turn".  Its error is |pos| * 2^-65 turns for every position an int32
+// holds, where pos * omega in fp32 would lose 2^-24 * pos * omega radians (6e-3 at
+// position 1e5).  The top 32 bits, as a signed fraction of half turns, go to sincospif.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+
+// Elements of pair j of a row: the rotated pairs first, then the elements that
+// pass through, two by two (j >= n in either layout).
+__device__ __forceinline__ int2 pair_elems(const RotaryTable& t, int j) {
+  if (t.half && j < t.n) return make_int2(j, j + t.n);
+  return make_int2(2 * j, 2 * j + 1);
+}
+
+__device__ __forceinline__ float2 pair_cos_sin(const RotaryTable& t, int j, const int* pos) {
+  const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos[t.axis[j]])) * t.turn[j];
+  float s, c;
+  sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
+  return make_float2(c, t.inverse ? -s : s);
+}
+
+template <typename T> struct Vec16;             // 16 bytes of T as fp32 values
+template <> struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(uint4 u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y); f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <> struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(uint4 u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t*>(&v);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Vec16<__half> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(uint4 u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t*>(&v);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }

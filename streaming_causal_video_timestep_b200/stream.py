@@ -322,3 +322,150 @@ def op_attention_fp8(q_codes, ks, vs, q_scale, k_scale, v_scale, out, out32=None
     ln = (c_int64 * n)(*[k.shape[1] for k in ks])
     check(lib.la_op_attention_fp8(_ptr(q_codes), Tq, H, d, n, kp, vp, ln, _ptr(q_scale), _ptr(k_scale),
                                   _ptr(v_scale), _ptr(out), _ptr(out32), _stream_handle(stream)))
+
+
+# ---- rotary positions with several axes, and the paged 8-bit cache ---------------------------
+_FLOATS = {torch.bfloat16: _lib.LA_BF16, torch.float16: _lib.LA_FP16, torch.float32: _lib.LA_FP32}
+
+
+def _rows(t, name, device=None, dtypes=_FLOATS):
+    """Checks a [tokens, heads, head_dim] tensor with contiguous head_dim; returns (pointer, token and head strides)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, head_dim]")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: head_dim must be contiguous, got strides {t.stride()}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr(), st, sh
+
+
+def _dense(t, dtype, shape, name, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _on(device, stream):
+    """The call's CUDA stream; the caller runs inside torch.cuda.device(device)."""
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"stream is on {s.device}, the tensors on {device}")
+    return s
+
+
+def _axes(pos, pairs, tokens, device):
+    """(pos pointer, number of axes, ctypes array) of a rotation."""
+    n = len(pairs)
+    return _dense(pos, torch.int32, (tokens, n), "pos", device), n, (c_int32 * n)(*pairs)
+
+
+def _cache(k_pages, v_pages, k_scale, v_scale, block_table, device):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise TypeError("k_pages must be a CUDA tensor [num_pages, heads, page_tokens, head_dim]")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise TypeError("block_table must be a CUDA tensor [batch, max_pages]")
+    num, heads, page, d = shape = k_pages.shape
+    batch, width = block_table.shape
+    return _lib.LaPagedCache(_dense(k_pages, torch.uint8, shape, "k_pages", device),
+                             _dense(v_pages, torch.uint8, shape, "v_pages", device),
+                             _dense(k_scale, torch.float32, (num, heads), "k_scale", device),
+                             _dense(v_scale, torch.float32, (num, heads), "v_scale", device),
+                             _dense(block_table, torch.int32, (batch, width), "block_table", device),
+                             num, heads, page, d, batch, width)
+
+
+def op_rope_axes(x, pos, pairs, out=None, theta=10000.0, half=False, inverse=False, stream=None):
+    """Rotary positions with several axes (la_op_rope_axes): x [tokens, heads, head_dim] bf16, fp16 or fp32
+    (any token and head strides), pos int32 [tokens, axes], pairs: rotary pairs of each axis.  half: pair i is
+    elements (i, i + n) instead of (2i, 2i+1).  inverse undoes the rotation: the gradient of x from that of
+    out.  out: a tensor like x (x itself: in place), made if None; returns out."""
+    lib = load()
+    px, xt, xh = _rows(x, "x")
+    dev = x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
+    po, ot, oh = _rows(out, "out", dev)
+    tokens, heads, d = x.shape
+    pp, n, arr = _axes(pos, pairs, tokens, dev)
+    with torch.cuda.device(dev):
+        check(lib.la_op_rope_axes(_FLOATS[x.dtype], px, xt, xh, po, ot, oh, tokens, heads, d, pp, n, arr, theta,
+                                  1 if half else 0, 1 if inverse else 0, _on(dev, stream).cuda_stream))
+    return out
+
+
+def op_cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, cache_len, cu_new, max_new, pos=None,
+                        pairs=None, theta=10000.0, half=False, stream=None):
+    """Appends keys (rotated by pos / pairs if given, as op_rope_axes) and values to a paged cache of e4m3 codes
+    with one power-of-two scale for each (page, head) (la_op_cache_append_fp8).  k, v [tokens, heads, head_dim];
+    k_pages, v_pages uint8 [num_pages, heads, page_tokens, head_dim]; k_scale, v_scale fp32 [num_pages, heads];
+    block_table int32 [batch, max_pages]; cache_len int32 [batch], tokens held before the call; cu_new int32
+    [batch + 1], each sequence's rows of k and v, at most max_new of them.  Writes pages and scales only."""
+    lib = load()
+    pk, kt, kh = _rows(k, "k")
+    dev = k.device
+    pv, vt, vh = _rows(v, "v", dev)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError(f"v: expected {k.dtype} {tuple(k.shape)}, got {v.dtype} {tuple(v.shape)}")
+    c = _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev)
+    tokens, heads, d = k.shape
+    if heads != c.heads or d != c.head_dim:
+        raise ValueError(f"k: expected [tokens, {c.heads}, {c.head_dim}], got {tuple(k.shape)}")
+    plen = _dense(cache_len, torch.int32, (c.batch,), "cache_len", dev)
+    pcu = _dense(cu_new, torch.int32, (c.batch + 1,), "cu_new", dev)
+    if (pos is None) != (pairs is None):
+        raise ValueError("pos and pairs go together")
+    pp, n, arr = _axes(pos, pairs, tokens, dev) if pos is not None else (None, 0, None)
+    with torch.cuda.device(dev):
+        check(lib.la_op_cache_append_fp8(ctypes.byref(c), _FLOATS[k.dtype], pk, kt, kh, pv, vt, vh, tokens, pcu, plen,
+                                         max_new, pp, n, arr, theta, 1 if half else 0, _on(dev, stream).cuda_stream))
+
+
+_HALVES = {torch.bfloat16: _lib.LA_BF16, torch.float16: _lib.LA_FP16}
+
+
+def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, cu_q, max_q, max_kv, out=None,
+                           out32=None, causal_block=0, scale=None, stream=None):
+    """Attention of a ragged batch over the paged e4m3 cache (la_op_attention_cache_fp8).  q [tokens, heads,
+    head_dim] bf16 or fp16, heads a multiple of the cache's; the cache as in op_cache_append_fp8; kv_len int32
+    [batch]; cu_q int32 [batch + 1], at most max_q rows each; max_kv: a bound of kv_len.  causal_block 0: every
+    key visible; c: a sequence's queries are its last tokens, in blocks of c that see themselves and all before.
+    scale: of the scores, 1/sqrt(head_dim) if None.  out: a tensor like q, made if None (zeros for rows that
+    see no key; rows of no sequence are not written); out32: optional fp32 [tokens, heads, head_dim].
+    Returns out."""
+    lib = load()
+    pq, qt, qh = _rows(q, "q", dtypes=_HALVES)
+    dev = q.device
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"out: expected {q.dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
+    po, ot, oh = _rows(out, "out", dev)
+    c = _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev)
+    tokens, heads, d = q.shape
+    if d != c.head_dim:
+        raise ValueError(f"q: expected head_dim {c.head_dim}, got {d}")
+    plen = _dense(kv_len, torch.int32, (c.batch,), "kv_len", dev)
+    pcu = _dense(cu_q, torch.int32, (c.batch + 1,), "cu_q", dev)
+    p32 = None if out32 is None else _dense(out32, torch.float32, q.shape, "out32", dev)
+    with torch.cuda.device(dev):
+        s = _on(dev, stream)
+        ref = ctypes.byref(c)
+        need = lib.la_op_attention_cache_fp8_workspace(ref, tokens, heads, max_q, max_kv)
+        if need < 0:
+            check(int(need))
+        ws = None
+        if need > 0:
+            with torch.cuda.stream(s):          # the allocator hands it out again behind this stream's work
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        check(lib.la_op_attention_cache_fp8(ref, _HALVES[q.dtype], pq, qt, qh, tokens, heads, pcu, plen, max_q, max_kv,
+                                            causal_block, d ** -0.5 if scale is None else scale, po, ot, oh, p32,
+                                            None if ws is None else ws.data_ptr(), need, s.cuda_stream))
+    return out
