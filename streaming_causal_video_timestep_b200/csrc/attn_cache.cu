@@ -131,7 +131,7 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     const int key0 = st * 16;
     const int pg = cache_page(p, b, key0);
     if (pg >= 0) {
-      load16<D>(p, pg, key0 % p.page_tokens, hk, keys - key0, lane, x);
+      load16<D>(p, pg, key0 & (p.page_tokens - 1), hk, keys - key0, lane, x);
       return;
     }
 #pragma unroll
@@ -296,20 +296,30 @@ k_attn_cache_join(const __grid_constant__ AttnCacheParams p) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const AttnCacheParams& p, cudaStream_t st) {
+cudaError_t launch_rows(const AttnCacheParams& p, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.max_q) * (p.heads / p.kv_heads);
   const long long gx = (rows + 15) / 16 * p.nsplit;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;
   k_attn_cache_rows<T, D><<<dim3(static_cast<unsigned>(gx), p.kv_heads, p.batch), WARPS * 32, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.nsplit == 1) return e;
-  k_attn_cache_join<T, D><<<ceil_div_i(static_cast<long long>(p.tokens) * p.heads, 4), 128, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const AttnCacheParams& p, cudaStream_t st) {
+  const long long all = static_cast<long long>(p.tokens) * p.heads;
+  if ((all + 3) / 4 > 0x7fffffffLL) return cudaErrorInvalidValue;
+  k_attn_cache_join<T, D><<<ceil_div_i(all, 4), 128, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_cache(int dtype, const AttnCacheParams& p, cudaStream_t st) {
-  if (dtype == LA_BF16) return p.d == 64 ? launch<__nv_bfloat16, 64>(p, st) : launch<__nv_bfloat16, 128>(p, st);
-  return p.d == 64 ? launch<__half, 64>(p, st) : launch<__half, 128>(p, st);
+cudaError_t launch_attn_cache_rows(int dtype, const AttnCacheParams& p, cudaStream_t st) {
+  if (dtype == LA_BF16) return p.d == 64 ? launch_rows<__nv_bfloat16, 64>(p, st) : launch_rows<__nv_bfloat16, 128>(p, st);
+  return p.d == 64 ? launch_rows<__half, 64>(p, st) : launch_rows<__half, 128>(p, st);
+}
+
+cudaError_t launch_attn_cache_join(int dtype, const AttnCacheParams& p, cudaStream_t st) {
+  if (dtype == LA_BF16) return p.d == 64 ? launch_join<__nv_bfloat16, 64>(p, st) : launch_join<__nv_bfloat16, 128>(p, st);
+  return p.d == 64 ? launch_join<__half, 64>(p, st) : launch_join<__half, 128>(p, st);
 }

@@ -38,7 +38,7 @@ __device__ __forceinline__ int cache_limit(const AttnCacheParams& p, const Cache
 }
 // Page of the sequence that holds key j (j < L), -1 (and the error word) if the table names none.
 __device__ __forceinline__ int cache_page(const AttnCacheParams& p, int b, int j) {
-  const int pg = p.block_table[static_cast<long long>(b) * p.max_pages + j / p.page_tokens];
+  const int pg = p.block_table[static_cast<long long>(b) * p.max_pages + (j >> p.page_shift)];
   if (pg >= 0 && pg < p.num_pages) return pg;
   raise_device_error(p.err, LA_DEVERR_BAD_DESC);
   return -1;

@@ -177,8 +177,14 @@ struct AttnCacheParams {
   const int* block_table; const int* kv_len; const int* cu_q;
   int tokens, batch, heads, kv_heads, d, page_tokens, num_pages, max_pages, max_q, causal_block;
   float scale_log2;                    // softmax scale * log2(e)
+  int page_shift;                      // log2(page_tokens)
+  int q_vec;                           // q's rows are 16-byte aligned
   int nsplit;                          // pieces of the key axis
   float* part_o; float2* part_ml;      // nsplit > 1: [nsplit, tokens, heads, d], [nsplit, tokens, heads]
   int* err;
 };
-cudaError_t launch_attn_cache(int dtype, const AttnCacheParams& p, cudaStream_t st);
+// Few rows (max_q * heads / kv_heads <= LA_CACHE_FEW_ROWS) and the join of split keys; many rows.
+#define LA_CACHE_FEW_ROWS 16
+cudaError_t launch_attn_cache_rows(int dtype, const AttnCacheParams& p, cudaStream_t st);
+cudaError_t launch_attn_cache_join(int dtype, const AttnCacheParams& p, cudaStream_t st);
+cudaError_t launch_attn_cache_tc(int dtype, const AttnCacheParams& p, cudaStream_t st);

@@ -59,13 +59,26 @@ bool cache_fine(const la_paged_cache* c) {
          static_cast<int64_t>(c->max_pages) * c->page_tokens <= kMaxRows;
 }
 
-// Pieces of the key axis: enough CTAs (16 rows each) for 3 on every SM, each with
-// at least 256 keys.
+bool few_rows(int64_t max_q, int32_t heads, int32_t kv_heads) { return max_q * (heads / kv_heads) <= LA_CACHE_FEW_ROWS; }
+
+// Pieces of the key axis.  Few rows: enough CTAs for 3 on every SM, each with at
+// least 256 keys.  Many rows (one CTA an SM, 256 rows each): the number of pieces
+// that makes the fewest key tiles in a row on the busiest SM, a piece counted two
+// tiles longer than it is for its start and end and its part of the join.
 int plan_split(int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
   const int64_t rows = max_q * (heads / kv_heads);
-  const int64_t ctas = (rows + 15) / 16 * kv_heads * batch;
-  const int64_t want = 148 * 3;
-  return static_cast<int>(std::max<int64_t>(1, std::min((want + ctas - 1) / std::max<int64_t>(ctas, 1), max_kv / 256)));
+  if (few_rows(max_q, heads, kv_heads)) {
+    const int64_t ctas = static_cast<int64_t>(kv_heads) * batch, want = 148 * 3;
+    return static_cast<int>(std::max<int64_t>(1, std::min((want + ctas - 1) / ctas, max_kv / 256)));
+  }
+  const int64_t ctas = (rows + 255) / 256 * kv_heads * batch, tiles = (max_kv + 127) / 128;
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int n = 1; n <= 32 && (n == 1 || tiles / n >= 4); ++n) {
+    const int64_t cost = (ctas * n + 147) / 148 * ((tiles + n - 1) / n + 2);
+    if (cost < best_cost) best_cost = cost, best = n;
+  }
+  return best;
 }
 
 }  // namespace
@@ -173,6 +186,7 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
   p.q = q;
   p.out = out;
   p.out32 = out32;
+  p.q_vec = aligned(q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
   p.q_st = q_token_stride;
   p.q_sh = q_head_stride;
   p.o_st = out_token_stride;
@@ -190,6 +204,7 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
   p.kv_heads = cache->heads;
   p.d = cache->head_dim;
   p.page_tokens = cache->page_tokens;
+  p.page_shift = p.page_tokens == 32 ? 5 : p.page_tokens == 64 ? 6 : 7;
   p.num_pages = cache->num_pages;
   p.max_pages = cache->max_pages;
   p.max_q = static_cast<int>(std::min(max_q, tokens));
@@ -201,7 +216,11 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
     p.part_ml = reinterpret_cast<float2*>(p.part_o + p.nsplit * tokens * heads * p.d);
   }
   if (op_error_word(&p.err) != LA_OK) return LA_ECUDA;
-  return ret(launch_attn_cache(dtype, p, static_cast<cudaStream_t>(cuda_stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = few_rows(p.max_q, heads, cache->heads) ? launch_attn_cache_rows(dtype, p, st)
+                                                         : launch_attn_cache_tc(dtype, p, st);
+  if (e == cudaSuccess && p.nsplit > 1) e = launch_attn_cache_join(dtype, p, st);
+  return ret(e);
 }
 
 }  // extern "C"
