@@ -653,7 +653,7 @@ int la_op_cache_append_fp8(const la_paged_cache* cache, int32_t dtype, const voi
  * the same arguments (0: may be NULL); calls that may run at the same time need
  * one each.  Results do not depend on what it holds.  A sequence or page that
  * does not fit the arrays is reported as by the append (its rows are not
- * written; keys of a bad page count as zero keys and values).
+ * written; keys of a bad page are not seen).
  */
 int64_t la_op_attention_cache_fp8_workspace(const la_paged_cache* cache, int64_t tokens,
                                             int32_t heads, int64_t max_q, int64_t max_kv);

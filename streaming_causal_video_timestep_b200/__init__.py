@@ -13,5 +13,6 @@ def __getattr__(name):
                 "op_attention_fp8", "op_rope_axes", "op_cache_append_fp8", "op_attention_cache_fp8", "torch_dtype",
                 "sched_trace"):
         from . import stream
-        return getattr(stream, name)
+        value = globals()[name] = getattr(stream, name)      # found at once from the next time on
+        return value
     raise AttributeError(name)

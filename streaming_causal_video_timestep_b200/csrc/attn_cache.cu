@@ -4,8 +4,10 @@
 // k_attn_cache_rows: one CTA takes 16 rows (query token x head of the key head's
 // group) and one piece of the keys; its 4 warps take 16 keys at a time in turn, each
 // with a running maximum and sum of its own, joined in shared memory at the end.
-// Bound: HBM, every K and V code read once (for up to 16 rows), straight into
-// registers in 16-byte loads, the next 16 keys' under way while these are used.
+// Bound: HBM, every K and V code read once (for up to 16 rows).  A warp keeps
+// STAGES - 1 steps of 16 keys (4 KB at D = 128) under way with cp.async into a ring
+// of its own, so no warp waits for another; 16-byte chunks are placed by chunk ^ row
+// so that the reads below meet no bank twice at D = 128.
 //
 // The products run on mma.sync m16n8k16 (fp16 operands, fp32 sums): at 16 rows the
 // tensor work is a quarter of what HBM allows, and the operands need no shared
@@ -15,8 +17,10 @@
 //     4i .. 4i+3 of them stands for head dims 16c + 4i + {0, 1 | 2, 3}; Q is laid out
 //     the same way once.
 //   O = P V: the MMA's n index lane / 4 stands for head dims (D/8) * n + jn of its
-//     jn-th tile, so a lane reads (D/8) consecutive bytes of its keys 2c, 2c+1, 8+2c,
-//     9+2c, which are the keys whose P it holds.
+//     jn-th tile, so a lane reads (D/8) consecutive bytes of the 4 keys whose P it
+//     holds.
+//   The n-th score column of an 8-key group stands for key n ^ 4 (n & 1) of it, which
+//     spreads the rows that one quarter warp reads over the swizzle in both products.
 // e4m3 codes are exact in fp16; q is scaled to fp16 by a power of two per row.  The
 // key page's scale multiplies the scores; the value page's scale enters P's exponent
 // (and leaves the normaliser again), so P V needs no multiplications of its own.
@@ -25,6 +29,7 @@
 namespace {
 
 constexpr int WARPS = 4;
+constexpr int STAGES = 4;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -33,44 +38,29 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 16 keys' codes of one lane.
-template <int D> struct Keys16 {
-  uint4 k[2][D / 64];        // key n of 8-key group nt: bytes 16c.. and 64 + 16c..
-  uint32_t v[4][D / 32];     // keys 2c, 2c+1, 8+2c, 9+2c: D/8 bytes
-  float ks, vs;              // scales of the page
-};
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
 
-template <int D>
-__device__ __forceinline__ void load16(const AttnCacheParams& p, int pg, int off, int hk, int valid, int lane, Keys16<D>& x) {
-  const int n = lane >> 2, c = lane & 3;
-  const long long plane = static_cast<long long>(pg) * p.kv_heads + hk;
-  const uint8_t* kp = p.k_pages + plane * (p.page_tokens * D) + static_cast<long long>(off) * D;
-  const uint8_t* vp = p.v_pages + plane * (p.page_tokens * D) + static_cast<long long>(off) * D;
-  x.ks = __ldg(p.k_scale + plane);
-  x.vs = __ldg(p.v_scale + plane);
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i)
-      x.k[nt][i] = __ldg(reinterpret_cast<const uint4*>(kp + (nt * 8 + n) * D + i * 64 + c * 16));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = (i >> 1) * 8 + 2 * c + (i & 1);
-    if constexpr (D == 128) {
-      uint4 w = __ldg(reinterpret_cast<const uint4*>(vp + key * D + n * 16));
-      if (key >= valid) w = make_uint4(0, 0, 0, 0);          // behind the last key: codes of any value
-      x.v[i][0] = w.x; x.v[i][1] = w.y; x.v[i][2] = w.z; x.v[i][3] = w.w;
-    } else {
-      uint2 w = __ldg(reinterpret_cast<const uint2*>(vp + key * D + n * 8));
-      if (key >= valid) w = make_uint2(0, 0);
-      x.v[i][0] = w.x; x.v[i][1] = w.y;
-    }
-  }
+// One step's 16 keys in shared memory: codes as [16][D], chunk ch of row r at slot
+// ch ^ (r & 7) (D = 128) or ch ^ (r / 2 & 3) (D = 64), and the page's scales.
+template <int D> struct Step {
+  uint8_t k[16 * D], v[16 * D];
+};
+template <int D> __device__ __forceinline__ int slot_of(int r, int ch) { return r * D + ((ch ^ (D == 128 ? r & 7 : r >> 1 & 3)) << 4); }
+
+template <int D> constexpr size_t rows_smem() {
+  const size_t ring = WARPS * STAGES * sizeof(Step<D>), join = WARPS * 16 * D * 4;
+  return ring > join ? ring : join;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(WARPS * 32)
+__global__ void __launch_bounds__(WARPS * 32, 3)
 k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
+  if (p.nsplit > 1) launch_dependents();    // the join may take its place; it waits for this grid's end
   const int b = blockIdx.z, hk = blockIdx.y;
   const int split = blockIdx.x % p.nsplit, tile = blockIdx.x / p.nsplit;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = lane >> 2, c = lane & 3;
@@ -79,6 +69,42 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
   const int G = p.heads / p.kv_heads;
   const int rows = s.n * G, r0 = tile * 16;
   if (r0 >= rows) return;
+
+  const int last = min(rows, r0 + 16) - 1;
+  const int keys = cache_limit(p, s, last / G);                 // limits do not fall along the rows
+  const int steps = (keys + 15) / 16;
+  const int per = (steps + p.nsplit - 1) / p.nsplit;
+  const int s0 = split * per, s1 = min(steps, s0 + per);
+
+  // The first steps' copies are under way while Q is brought in.
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  __shared__ float2 scales[WARPS][STAGES];
+  Step<D>* ring = reinterpret_cast<Step<D>*>(ring_raw) + warp * STAGES;
+  // Page of step st (-1: behind the end, or none): looked up one step before its copies start.
+  auto page_of = [&](int st) { return st < s1 ? cache_page(p, b, st * 16) : -1; };
+  auto fetch = [&](int st, int pg, int slot) {
+    if (st < s1) {
+      const bool on = pg >= 0;
+      const long long plane = static_cast<long long>(on ? pg : 0) * p.kv_heads + hk;
+      const long long at = plane * (p.page_tokens * D) + (st * 16 & (p.page_tokens - 1)) * D;
+      const int valid = on ? keys - st * 16 : 0;             // rows behind the last key become zeros
+      Step<D>& x = ring[slot];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int q = i * 32 + lane, r = q / (D / 16), ch = q % (D / 16);
+        cp_async16(x.k + slot_of<D>(r, ch), p.k_pages + at + q * 16, r < valid);
+        cp_async16(x.v + slot_of<D>(r, ch), p.v_pages + at + q * 16, r < valid);
+      }
+      if (lane < 2) cp_async4(lane ? &scales[warp][slot].y : &scales[warp][slot].x, (lane ? p.v_scale : p.k_scale) + plane, on);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");     // one group a step, empty ones too
+  };
+  int st = s0 + warp, pg = page_of(st);
+  for (int i = 0; i < STAGES - 1; ++i) {
+    const int nx = page_of(st + (i + 1) * WARPS);
+    fetch(st + i * WARPS, pg, i);
+    pg = nx;
+  }
 
   // Q: rows n and n + 8 of the tile, as MMA operands; sc[]: log2(e)-scaled softmax
   // scale of the row over the power of two that its q carries.
@@ -95,12 +121,22 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     float f[D / 64][16];
     uint32_t amax = 0;
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j)
+    for (int j = 0; j < D / 64; ++j) {
+      if (p.q_vec) {
+        uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (on) {
+          u[0] = __ldg(reinterpret_cast<const uint4*>(q + j * 64 + c * 16));
+          u[1] = __ldg(reinterpret_cast<const uint4*>(q + j * 64 + c * 16) + 1);
+        }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        f[j][e] = on ? q_to_f32(q[j * 64 + c * 16 + e]) : 0.f;
-        amax = max(amax, __float_as_uint(f[j][e]) & 0x7fffffffu);
+        for (int e = 0; e < 16; ++e) f[j][e] = q_to_f32(reinterpret_cast<const T*>(u)[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[j][e] = on ? q_to_f32(q[j * 64 + c * 16 + e]) : 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(f[j][e]) & 0x7fffffffu);
+    }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const float g = q_row_scale(amax);
@@ -113,12 +149,6 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
         qa[j * 4 + e][2 + i] = pack_f16x2(f[j][4 * e + 2] * g, f[j][4 * e + 3] * g);
       }
   }
-  const int last = min(rows, r0 + 16) - 1;
-  const int keys = cache_limit(p, s, last / G);                 // limits do not fall along the rows
-  const int steps = (keys + 15) / 16;
-  const int per = (steps + p.nsplit - 1) / p.nsplit;
-  const int s0 = split * per, s1 = min(steps, s0 + per);
-
   float o[D / 8][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -126,51 +156,39 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-  Keys16<D> cur, nxt;
-  auto fetch = [&](int st, Keys16<D>& x) {
-    const int key0 = st * 16;
-    const int pg = cache_page(p, b, key0);
-    if (pg >= 0) {
-      load16<D>(p, pg, key0 & (p.page_tokens - 1), hk, keys - key0, lane, x);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) x.k[i][j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) x.v[i][j] = 0;
-    x.ks = x.vs = 1.0f;
-  };
-  int st = s0 + warp;
-  if (st < s1) fetch(st, cur);
-  for (; st < s1; st += WARPS) {
-    if (st + WARPS < s1) fetch(st + WARPS, nxt);
+  for (int slot = 0; st < s1; st += WARPS, slot = (slot + 1) % STAGES) {
+    const int ahead = st + (STAGES - 1) * WARPS;
+    const int nx = page_of(ahead + WARPS);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    __syncwarp();                                            // every lane's copies of this step, and its reads of the last one
+    fetch(ahead, pg, (slot + STAGES - 1) % STAGES);
+    pg = nx;
+    const Step<D>& cur = ring[slot];
+    const float ks = scales[warp][slot].x, vs = scales[warp][slot].y;
     float x[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        const uint32_t w[4] = {cur.k[nt][j].x, cur.k[nt][j].y, cur.k[nt][j].z, cur.k[nt][j].w};
+        const uint4 u = *reinterpret_cast<const uint4*>(cur.k + slot_of<D>(nt * 8 + (n ^ (n & 1) << 2), 4 * j + c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           mma16816(x[nt], qa[j * 4 + e], e4m3x2_f16x2_lo(w[e]), e4m3x2_f16x2_hi(w[e]));
       }
     }
-    // x[nt][2 i + e]: row n + 8 i, key 8 nt + 2 c + e
-    const float lv = log2f(cur.vs), rv = 1.0f / cur.vs;
+    // x[nt][2 i + e]: row n + 8 i, key 8 nt + ((2 c + e) ^ 4 e)
+    const float lv = __log2f(vs), rv = __frcp_rn(vs);
     float mt[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float a = sc[i] * cur.ks;
+      const float a = sc[i] * ks;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int key = st * 16 + nt * 8 + 2 * c + e;
+          const int key = st * 16 + nt * 8 + ((2 * c + e) ^ e << 2);
           x[nt][2 * i + e] = key < lim[i] ? fmaf(x[nt][2 * i + e], a, lv) : -INFINITY;
         }
       mt[i] = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
@@ -204,21 +222,34 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
       pa[i] = pack_f16x2(e[0], e[1]);
       pa[2 + i] = pack_f16x2(e[2], e[3]);
     }
+    uint32_t vw[4][D / 32];                                           // D/8 bytes of the lane's 4 keys
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (i >> 1) * 8 + ((2 * c + (i & 1)) ^ (i & 1) << 2);
+      if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(cur.v + slot_of<D>(r, n));
+        vw[i][0] = u.x; vw[i][1] = u.y; vw[i][2] = u.z; vw[i][3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(cur.v + slot_of<D>(r, n >> 1) + (n & 1) * 8);
+        vw[i][0] = u.x; vw[i][1] = u.y;
+      }
+    }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {                                // 4 bytes of each of the 4 keys
-      const uint32_t a01 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140), a23 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
-      const uint32_t b01 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140), b23 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
+      const uint32_t a01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a23 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+      const uint32_t b01 = __byte_perm(vw[2][w], vw[3][w], 0x5140), b23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
       mma16816(o[4 * w + 0], pa, e4m3x2_f16x2_lo(a01), e4m3x2_f16x2_lo(b01));
       mma16816(o[4 * w + 1], pa, e4m3x2_f16x2_hi(a01), e4m3x2_f16x2_hi(b01));
       mma16816(o[4 * w + 2], pa, e4m3x2_f16x2_lo(a23), e4m3x2_f16x2_lo(b23));
       mma16816(o[4 * w + 3], pa, e4m3x2_f16x2_hi(a23), e4m3x2_f16x2_hi(b23));
     }
-    cur = nxt;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 
   // Join the warps: o[j][2 i + e] is row n + 8 i, head dim (D/8) (2 c + e) + j.
   __shared__ float sm[WARPS][16], sl[WARPS][16];
-  __shared__ float so[WARPS][16][D];
+  float(*so)[16][D] = reinterpret_cast<float(*)[16][D]>(ring_raw);   // [WARPS][16][D], over the rings
+  __syncthreads();                                                    // no warp reads its ring any more
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -228,14 +259,13 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
       sl[warp][n + 8 * i] = l[i];
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2 && r0 + n + 8 * i < rows; ++e)
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) so[warp][n + 8 * i][(D / 8) * (2 * c + e) + j] = o[j][2 * i + e];
   }
   __syncthreads();
-  for (int q = threadIdx.x; q < 16 * (D / 4); q += WARPS * 32) {
+  for (int q = threadIdx.x; q < min(16, rows - r0) * (D / 4); q += WARPS * 32) {
     const int r = q / (D / 4), d4 = q % (D / 4) * 4;
-    if (r0 + r >= rows) continue;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm[w][r]);
@@ -258,15 +288,18 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
   }
 }
 
-// One warp joins the pieces of one (token, head) row: o = sum o_s 2^(m_s - M) / sum l_s 2^(m_s - M).
+// Joins the pieces of (token, head) rows: o = sum o_s 2^(m_s - M) / sum l_s 2^(m_s - M).
+// `wpr` warps of a CTA's 8 share a row, each with its pieces' own maximum, and the
+// first of them joins what they found.  A lane holds 4 head dims.
+constexpr int JOIN_WARPS = 8;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128)
-k_attn_cache_join(const __grid_constant__ AttnCacheParams p) {
-  const long long row = blockIdx.x * 4LL + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(JOIN_WARPS * 32)
+k_attn_cache_join(const __grid_constant__ AttnCacheParams p, int wpr) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = warp % wpr;
+  const long long row = blockIdx.x * static_cast<long long>(JOIN_WARPS / wpr) + warp / wpr;
   const long long all = static_cast<long long>(p.tokens) * p.heads;
-  if (row >= all) return;
-  const int tok = static_cast<int>(row / p.heads), head = static_cast<int>(row % p.heads);
+  const int tok = static_cast<int>(min(row, all - 1) / p.heads), head = static_cast<int>(min(row, all - 1) % p.heads);
   // Rows of no sequence stay as they are.
   int lo = 0, hi = p.batch;
   while (lo < hi) {                               // first b with cu_q[b + 1] > tok
@@ -274,25 +307,53 @@ k_attn_cache_join(const __grid_constant__ AttnCacheParams p) {
     if (p.cu_q[mid + 1] > tok) hi = mid;
     else lo = mid + 1;
   }
-  if (lo == p.batch) return;
-  const CacheSeq s = cache_seq(p, lo);
-  if (s.bad || tok < s.q0 || tok >= s.q0 + s.n) return;
-  float M = -INFINITY;
-  for (int i = lane; i < p.nsplit; i += 32) M = fmaxf(M, p.part_ml[i * all + row].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+  bool on = row < all && lo < p.batch;
+  if (on) {
+    const CacheSeq s = cache_seq(p, lo);
+    on = !s.bad && tok >= s.q0 && tok < s.q0 + s.n;
+  }
+  grid_dependency_wait();
+  float M = -INFINITY, L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
   const int d4 = lane * 4;
-  for (int i = 0; i < p.nsplit; ++i) {
-    const float2 ml = p.part_ml[i * all + row];
-    const float f = ml.x == M ? 1.0f : fast_exp2(ml.x - M);
-    L += ml.y * f;
-    if (d4 < D) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (i * all + row) * D + d4);
+  if (on) {
+    const float2* ml = p.part_ml + row;
+    const float* po = p.part_o + row * D + d4;
+    for (int i = part + lane * wpr; i < p.nsplit; i += 32 * wpr) M = fmaxf(M, ml[i * all].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+    for (int i = part; i < p.nsplit; i += wpr) {
+      const float2 w = ml[i * all];
+      const float f = w.x == M ? 1.0f : fast_exp2(w.x - M);
+      L += w.y * f;
+      if (d4 < D) {
+        const float4 v = *reinterpret_cast<const float4*>(po + i * all * D);
+        a[0] += v.x * f; a[1] += v.y * f; a[2] += v.z * f; a[3] += v.w * f;
+      }
+    }
+  }
+  if (wpr > 1) {
+    __shared__ float sm[JOIN_WARPS], sl[JOIN_WARPS];
+    __shared__ float4 so[JOIN_WARPS][32];
+    if (lane == 0) {
+      sm[warp] = M;
+      sl[warp] = L;
+    }
+    so[warp][lane] = make_float4(a[0], a[1], a[2], a[3]);
+    __syncthreads();
+    if (part != 0) return;
+    float X = M;
+    for (int w = 1; w < wpr; ++w) X = fmaxf(X, sm[warp + w]);
+    L = 0.f;
+    a[0] = a[1] = a[2] = a[3] = 0.f;
+    for (int w = 0; w < wpr; ++w) {
+      const float f = sm[warp + w] == X ? 1.0f : fast_exp2(sm[warp + w] - X);
+      const float4 v = so[warp + w][lane];
+      L += sl[warp + w] * f;
       a[0] += v.x * f; a[1] += v.y * f; a[2] += v.z * f; a[3] += v.w * f;
     }
   }
-  if (d4 < D) cache_store4<T>(p, tok, head, d4, a, L);
+  if (on && d4 < D) cache_store4<T>(p, tok, head, d4, a, L);
 }
 
 template <typename T, int D>
@@ -300,16 +361,30 @@ cudaError_t launch_rows(const AttnCacheParams& p, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.max_q) * (p.heads / p.kv_heads);
   const long long gx = (rows + 15) / 16 * p.nsplit;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;
-  k_attn_cache_rows<T, D><<<dim3(static_cast<unsigned>(gx), p.kv_heads, p.batch), WARPS * 32, 0, st>>>(p);
+  auto kern = k_attn_cache_rows<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(rows_smem<D>()));
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(static_cast<unsigned>(gx), p.kv_heads, p.batch), WARPS * 32, rows_smem<D>(), st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const AttnCacheParams& p, cudaStream_t st) {
-  const long long all = static_cast<long long>(p.tokens) * p.heads;
-  if ((all + 3) / 4 > 0x7fffffffLL) return cudaErrorInvalidValue;
-  k_attn_cache_join<T, D><<<ceil_div_i(all, 4), 128, 0, st>>>(p);
-  return cudaGetLastError();
+  int wpr = 1;
+  while (wpr < JOIN_WARPS && p.nsplit > 4 * wpr) wpr *= 2;
+  const long long ctas = (static_cast<long long>(p.tokens) * p.heads * wpr + JOIN_WARPS - 1) / JOIN_WARPS;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // Launched while the pieces still run (they say when); waits for their end on the GPU.
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attn_cache_join<T, D>, p, wpr);
 }
 
 }  // namespace

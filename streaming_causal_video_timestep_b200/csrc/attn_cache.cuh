@@ -13,6 +13,11 @@
 #define LA_CACHE_P_BIAS 11.0f
 #define LA_CACHE_P_TAU 4.0f
 
+// Programmatic launch: the next grid of the stream may start, and waits here for the
+// end of the grid before it.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One sequence's place in the batch, checked: whatever the device arrays hold,
 // rows and keys stay inside the tensors.
 struct CacheSeq {

@@ -134,6 +134,7 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ volatile int abort_flag;
 
+  if (p.nsplit > 1) launch_dependents();
   const int b = blockIdx.z, hk = blockIdx.y;
   const int split = blockIdx.x % p.nsplit;
   const int pair = gridDim.x / p.nsplit - 1 - blockIdx.x / p.nsplit;   // under a causal mask the last rows have the most keys
@@ -300,7 +301,7 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
         if (lane < 4) {
           const int key = (t0 + t) * 128 + 32 * lane;
           const int x = lane == 0 ? pg[0] : lane == 1 ? pg[1] : lane == 2 ? pg[2] : pg[3];
-          float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+          float4 v = make_float4(1.f, -INFINITY, 0.f, 0.f);   // keys of no page are not seen
           if (x >= 0 && key < keys) {
             const long long plane = static_cast<long long>(x) * p.kv_heads + hk;
             const float vs = __ldg(p.v_scale + plane);

@@ -25,7 +25,8 @@ size_t elem_size(int32_t dtype) { return dtype == LA_FP32 ? 4 : 2; }
 bool known_dtype(int32_t dtype) { return dtype == LA_BF16 || dtype == LA_FP32 || dtype == LA_FP16; }
 
 // omega_{a,j} = theta^(-j / pairs[a]), as a fraction of a turn in units of 2^-64.
-// long double keeps all 64 bits that the product with a position uses.
+// long double keeps the 64 bits that the product with a position uses; every 8th
+// power is a powl, the others 7 multiplications at most from it (8 * 2^-64 relative).
 bool fill_table(RotaryTable& t, int32_t d, int32_t naxes, const int32_t* pairs, double theta, int32_t half,
                 int32_t inverse) {
   t.n = 0;
@@ -37,9 +38,12 @@ bool fill_table(RotaryTable& t, int32_t d, int32_t naxes, const int32_t* pairs, 
   constexpr long double two_pi = 6.283185307179586476925286766559005768L;
   for (int a = 0; a < naxes; ++a) {
     if (pairs[a] < 0 || pairs[a] > d / 2 - t.n) return false;
+    if (pairs[a] == 0) continue;
+    const long double step = powl(theta, -1.0L / pairs[a]);
+    long double turns = 0.0L;
     for (int j = 0; j < pairs[a]; ++j) {
-      const long double turns = powl(theta, -static_cast<long double>(j) / pairs[a]) / two_pi;   // <= 1 / (2 pi)
-      t.turn[t.n] = static_cast<unsigned long long>(roundl(ldexpl(turns, 64)));
+      turns = j % 8 == 0 ? powl(theta, -static_cast<long double>(j) / pairs[a]) / two_pi : turns * step;
+      t.turn[t.n] = static_cast<unsigned long long>(ldexpl(turns, 64));      // turns <= 1 / (2 pi)
       t.axis[t.n++] = static_cast<unsigned char>(a);
     }
   }
@@ -61,15 +65,18 @@ bool cache_fine(const la_paged_cache* c) {
 
 bool few_rows(int64_t max_q, int32_t heads, int32_t kv_heads) { return max_q * (heads / kv_heads) <= LA_CACHE_FEW_ROWS; }
 
-// Pieces of the key axis.  Few rows: enough CTAs for 3 on every SM, each with at
-// least 256 keys.  Many rows (one CTA an SM, 256 rows each): the number of pieces
-// that makes the fewest key tiles in a row on the busiest SM, a piece counted two
-// tiles longer than it is for its start and end and its part of the join.
+// Pieces of the key axis.  Few rows: enough CTAs for 3 on every SM with at least 128
+// keys each (16 streams of one token over 1561 keys: 9.7 us; 10.9 with 256), and
+// pieces of about 2048 keys where that makes more, which evens out ragged lengths
+// (16 x 40 heads over up to 14040 keys: 258 us; 343 unsplit, 285 with 1024 keys).
+// Many rows (one CTA an SM, 256 rows each): the number of pieces that makes the
+// fewest key tiles in a row on the busiest SM, a piece counted two tiles longer than
+// it is for its start and end and its part of the join.
 int plan_split(int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
   const int64_t rows = max_q * (heads / kv_heads);
   if (few_rows(max_q, heads, kv_heads)) {
     const int64_t ctas = static_cast<int64_t>(kv_heads) * batch, want = 148 * 3;
-    return static_cast<int>(std::max<int64_t>(1, std::min((want + ctas - 1) / ctas, max_kv / 256)));
+    return static_cast<int>(std::max({int64_t{1}, std::min((want + ctas - 1) / ctas, max_kv / 128), max_kv / 2048}));
   }
   const int64_t ctas = (rows + 255) / 256 * kv_heads * batch, tiles = (max_kv + 127) / 128;
   int best = 1;

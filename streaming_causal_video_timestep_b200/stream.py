@@ -326,10 +326,12 @@ def op_attention_fp8(q_codes, ks, vs, q_scale, k_scale, v_scale, out, out32=None
 
 # ---- rotary positions with several axes, and the paged 8-bit cache ---------------------------
 _FLOATS = {torch.bfloat16: _lib.LA_BF16, torch.float16: _lib.LA_FP16, torch.float32: _lib.LA_FP32}
+_HALVES = {torch.bfloat16: _lib.LA_BF16, torch.float16: _lib.LA_FP16}
 
 
-def _rows(t, name, device=None, dtypes=_FLOATS):
-    """Checks a [tokens, heads, head_dim] tensor with contiguous head_dim; returns (pointer, token and head strides)."""
+def _rows(t, name, dev=None, dtypes=_FLOATS):
+    """Checks a [tokens, heads, head_dim] tensor with contiguous head_dim; returns (pointer, token and head strides).
+    dev: the index of the device that it has to be on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
         raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, head_dim]")
     if t.dtype not in dtypes:
@@ -337,47 +339,66 @@ def _rows(t, name, device=None, dtypes=_FLOATS):
     st, sh, sd = t.stride()
     if sd != 1 and t.shape[2] != 1:
         raise ValueError(f"{name}: head_dim must be contiguous, got strides {t.stride()}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     return t.data_ptr(), st, sh
 
 
-def _dense(t, dtype, shape, name, device):
+def _dense(t, dtype, shape, name, dev):
+    """Checks a contiguous tensor on CUDA device `dev` (an index); returns its pointer."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _on(device, stream):
-    """The call's CUDA stream; the caller runs inside torch.cuda.device(device)."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"stream is on {s.device}, the tensors on {device}")
-    return s
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream handle) with `dev` the current device, on `stream` or the device's current one."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code != _lib.LA_OK:
+        check(code)
 
 
-def _axes(pos, pairs, tokens, device):
+def _axes(pos, pairs, tokens, dev):
     """(pos pointer, number of axes, ctypes array) of a rotation."""
     n = len(pairs)
-    return _dense(pos, torch.int32, (tokens, n), "pos", device), n, (c_int32 * n)(*pairs)
+    return _dense(pos, torch.int32, (tokens, n), "pos", dev), n, (c_int32 * n)(*pairs)
 
 
-def _cache(k_pages, v_pages, k_scale, v_scale, block_table, device):
+def _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev):
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise TypeError("k_pages must be a CUDA tensor [num_pages, heads, page_tokens, head_dim]")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise TypeError("block_table must be a CUDA tensor [batch, max_pages]")
     num, heads, page, d = shape = k_pages.shape
-    batch, width = block_table.shape
-    return _lib.LaPagedCache(_dense(k_pages, torch.uint8, shape, "k_pages", device),
-                             _dense(v_pages, torch.uint8, shape, "v_pages", device),
-                             _dense(k_scale, torch.float32, (num, heads), "k_scale", device),
-                             _dense(v_scale, torch.float32, (num, heads), "v_scale", device),
-                             _dense(block_table, torch.int32, (batch, width), "block_table", device),
+    batch, width = wide = block_table.shape
+    flat = (num, heads)
+    return _lib.LaPagedCache(_dense(k_pages, torch.uint8, shape, "k_pages", dev),
+                             _dense(v_pages, torch.uint8, shape, "v_pages", dev),
+                             _dense(k_scale, torch.float32, flat, "k_scale", dev),
+                             _dense(v_scale, torch.float32, flat, "v_scale", dev),
+                             _dense(block_table, torch.int32, wide, "block_table", dev),
                              num, heads, page, d, batch, width)
+
+
+def _like(x, out, name="out"):
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"{name}: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
+    return out
 
 
 def op_rope_axes(x, pos, pairs, out=None, theta=10000.0, half=False, inverse=False, stream=None):
@@ -387,17 +408,13 @@ def op_rope_axes(x, pos, pairs, out=None, theta=10000.0, half=False, inverse=Fal
     out.  out: a tensor like x (x itself: in place), made if None; returns out."""
     lib = load()
     px, xt, xh = _rows(x, "x")
-    dev = x.device
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
+    dev = x.get_device()
+    out = _like(x, out)
     po, ot, oh = _rows(out, "out", dev)
     tokens, heads, d = x.shape
     pp, n, arr = _axes(pos, pairs, tokens, dev)
-    with torch.cuda.device(dev):
-        check(lib.la_op_rope_axes(_FLOATS[x.dtype], px, xt, xh, po, ot, oh, tokens, heads, d, pp, n, arr, theta,
-                                  1 if half else 0, 1 if inverse else 0, _on(dev, stream).cuda_stream))
+    _call(lib.la_op_rope_axes, dev, stream, _FLOATS[x.dtype], px, xt, xh, po, ot, oh, tokens, heads, d, pp, n, arr, theta,
+          1 if half else 0, 1 if inverse else 0)
     return out
 
 
@@ -410,25 +427,22 @@ def op_cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, c
     [batch + 1], each sequence's rows of k and v, at most max_new of them.  Writes pages and scales only."""
     lib = load()
     pk, kt, kh = _rows(k, "k")
-    dev = k.device
+    dev = k.get_device()
     pv, vt, vh = _rows(v, "v", dev)
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError(f"v: expected {k.dtype} {tuple(k.shape)}, got {v.dtype} {tuple(v.shape)}")
+    shape = k.shape
+    if v.shape != shape or v.dtype != k.dtype:
+        raise ValueError(f"v: expected {k.dtype} {tuple(shape)}, got {v.dtype} {tuple(v.shape)}")
     c = _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev)
-    tokens, heads, d = k.shape
+    tokens, heads, d = shape
     if heads != c.heads or d != c.head_dim:
-        raise ValueError(f"k: expected [tokens, {c.heads}, {c.head_dim}], got {tuple(k.shape)}")
+        raise ValueError(f"k: expected [tokens, {c.heads}, {c.head_dim}], got {tuple(shape)}")
     plen = _dense(cache_len, torch.int32, (c.batch,), "cache_len", dev)
     pcu = _dense(cu_new, torch.int32, (c.batch + 1,), "cu_new", dev)
     if (pos is None) != (pairs is None):
         raise ValueError("pos and pairs go together")
     pp, n, arr = _axes(pos, pairs, tokens, dev) if pos is not None else (None, 0, None)
-    with torch.cuda.device(dev):
-        check(lib.la_op_cache_append_fp8(ctypes.byref(c), _FLOATS[k.dtype], pk, kt, kh, pv, vt, vh, tokens, pcu, plen,
-                                         max_new, pp, n, arr, theta, 1 if half else 0, _on(dev, stream).cuda_stream))
-
-
-_HALVES = {torch.bfloat16: _lib.LA_BF16, torch.float16: _lib.LA_FP16}
+    _call(lib.la_op_cache_append_fp8, dev, stream, ctypes.byref(c), _FLOATS[k.dtype], pk, kt, kh, pv, vt, vh, tokens, pcu,
+          plen, max_new, pp, n, arr, theta, 1 if half else 0)
 
 
 def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, kv_len, cu_q, max_q, max_kv, out=None,
@@ -441,12 +455,9 @@ def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, k
     see no key; rows of no sequence are not written); out32: optional fp32 [tokens, heads, head_dim].
     Returns out."""
     lib = load()
-    pq, qt, qh = _rows(q, "q", dtypes=_HALVES)
-    dev = q.device
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError(f"out: expected {q.dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
+    pq, qt, qh = _rows(q, "q", None, _HALVES)
+    dev = q.get_device()
+    out = _like(q, out)
     po, ot, oh = _rows(out, "out", dev)
     c = _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev)
     tokens, heads, d = q.shape
@@ -455,17 +466,18 @@ def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, k
     plen = _dense(kv_len, torch.int32, (c.batch,), "kv_len", dev)
     pcu = _dense(cu_q, torch.int32, (c.batch + 1,), "cu_q", dev)
     p32 = None if out32 is None else _dense(out32, torch.float32, q.shape, "out32", dev)
-    with torch.cuda.device(dev):
-        s = _on(dev, stream)
-        ref = ctypes.byref(c)
-        need = lib.la_op_attention_cache_fp8_workspace(ref, tokens, heads, max_q, max_kv)
-        if need < 0:
-            check(int(need))
-        ws = None
-        if need > 0:
-            with torch.cuda.stream(s):          # the allocator hands it out again behind this stream's work
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        check(lib.la_op_attention_cache_fp8(ref, _HALVES[q.dtype], pq, qt, qh, tokens, heads, pcu, plen, max_q, max_kv,
-                                            causal_block, d ** -0.5 if scale is None else scale, po, ot, oh, p32,
-                                            None if ws is None else ws.data_ptr(), need, s.cuda_stream))
+    ref = ctypes.byref(c)
+    need = lib.la_op_attention_cache_fp8_workspace(ref, tokens, heads, max_q, max_kv)
+    if need < 0:
+        check(int(need))
+    ws = None
+    if need > 0:
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):     # the allocator hands it out again behind that stream's work
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call(lib.la_op_attention_cache_fp8, dev, stream, ref, _HALVES[q.dtype], pq, qt, qh, tokens, heads, pcu, plen, max_q,
+          max_kv, causal_block, d ** -0.5 if scale is None else scale, po, ot, oh, p32, None if ws is None else ws.data_ptr(),
+          need)
     return out
