@@ -3,18 +3,21 @@
 //
 // One CTA = up to 256 rows (query token x head of the key head's group) of one
 // sequence and key head, over one piece of the keys in tiles of 128.  16 warps:
+//   warp 0       looks up pages and scales and brings the codes: one bulk copy (TMA)
+//                per page and tile, since a page's head is one run of bytes
 //   warp 1       owns tensor memory (512 columns: S_A | S_B | O_A | O_B) and issues
 //                the MMAs: PV_A(t), S_A(t+1), PV_B(t), S_B(t+1), ..., so that one
-//                tile's softmax runs beside the other's products; warps 0, 2, 3 idle
+//                tile's softmax runs beside the other's products; warps 2, 3 idle
 //   warps 4-11   softmax of tiles A and B, a thread a row; before that they bring Q
 //                to shared memory as fp16 under a power of two per row
-//   warps 12-15  bring K and V: 16-byte loads of e4m3 codes (page by page, so the
-//                page table costs a lookup per 32 keys), one tile ahead in registers,
-//                turned into fp16 (exactly) and written to a two-stage ring in the
-//                128-byte-swizzled layout that the MMAs read
+//   warps 12-15  unpack a tile's codes into fp16 (exactly), in the 128-byte-swizzled
+//                layout that the MMAs read, and hand it to them in a ring
 // The codes are unpacked once for 256 rows; at 64 conversions a clock and SM that
 // takes a quarter of the tile's MMA time and runs beside it.  fp16 operands keep q
-// and the codes exact and P to 11 bits (e4m3 or bf16 P would not).
+// and the codes exact and P to 11 bits (e4m3 or bf16 P would not).  Threads that
+// loaded the codes themselves lost more than they saved: the proxy fence behind each
+// tile waits for the loads that are under way for the next one (1.96 ms against
+// 1.57 ms at 4680 x 15600 x 40 x 128).
 //
 // Scales: the score of a key is acc * ks * (row factor); log2(vs) enters the
 // exponent, so a page's P carries its value scale and the normaliser takes it out
@@ -28,19 +31,19 @@ namespace {
 
 constexpr int THREADS = 512;
 constexpr int LAUNCH_REGS = 128;            // 65536 / 512
-constexpr int REGS_LOW = 40;                // warps 0-3
+constexpr int REGS_LOW = 56;                // warps 0-3
 constexpr int REGS_LOAD = 104;              // warps 12-15
-constexpr int REGS_SOFT = 184;              // warps 4-11
+constexpr int REGS_SOFT = 176;              // warps 4-11
 static_assert(128 * (REGS_LOW + REGS_LOAD + 2 * REGS_SOFT) <= THREADS * LAUNCH_REGS, "register split exceeds the launch");
 constexpr uint32_t BOX = 16384;             // 128 rows x 64 fp16, 128-byte swizzle
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int NSC = 8;                      // ring of the tiles' scales, longer than any K ring
-static_assert(NSC > 4, "the scales' ring must outlast the K ring");
+constexpr int NSC = 8;                      // ring of the tiles' scales
+static_assert(NSC >= 4 + 2, "the scales outlast the K ring and the tile of codes before it");
 
 template <int D> __host__ __device__ constexpr uint32_t tile_bytes() { return D / 64 * BOX; }
 template <int D> __host__ __device__ constexpr int stages() { return D == 64 ? 4 : 2; }
 template <int D> __host__ __device__ constexpr size_t smem_bytes() {
-  return 1024 + 2 * tile_bytes<D>() + stages<D>() * 2 * tile_bytes<D>() + NSC * 64 + 512;
+  return 1024 + 2 * tile_bytes<D>() + stages<D>() * 2 * tile_bytes<D>() + 2 * 128 * D + NSC * 64 + 512;
 }
 
 template <int N>
@@ -57,30 +60,53 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// One row's scores of a key tile (raw accumulators in s) to P (fp16 pairs) and the
-// row's share of the normaliser.  sc[c]: the 32-key chunk's (ks, log2 vs, 1 / vs).
+// Bytes from global to shared memory (16-byte aligned, a multiple of 16), counted on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Waits for this warp's tensor-memory loads; u is used behind it only.
+__device__ __forceinline__ void ld_wait(uint32_t (&u)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]), "+r"(u[8]),
+                 "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]), "+r"(u[16]),
+                 "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]), "+r"(u[24]),
+                 "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31])::"memory");
+}
+
+// One row's scores of a key tile (raw accumulators in tensor memory) to P (fp16
+// pairs), written over them, and the row's share of the normaliser.  The scores are
+// read twice, 32 at a time, once for the maximum: 128 of them held at once would not
+// fit beside the loaders' registers (chunk c of P lies in chunk c / 2 of the scores,
+// which the second pass has read by then).  sc[c]: the chunk's (ks, log2 vs, 1 / vs).
 template <bool MASKED>
-__device__ __forceinline__ float softmax_tile(float (&s)[128], uint32_t (&P)[64], int valid, float rowf, const float4* sc,
-                                              float& m_ref, float& alpha, bool& need) {
-  float a[4], lv[4], rv[4], mt = -INFINITY;
+__device__ __forceinline__ float softmax_tile(uint32_t s_base, int valid, float rowf, const float4* sc, float& m_ref,
+                                              float& alpha) {
+  uint32_t u[2][32];
+  float a[4], mt = -INFINITY;
+  tmem_ld32(s_base, u[0]);
+  ld_wait(u[0]);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float4 v = sc[c];
-    a[c] = v.x * rowf;
-    lv[c] = v.y;
-    rv[c] = v.z;
-    if (MASKED) {
+    tmem_ld32(s_base + (c + 1) % 4 * 32, u[(c + 1) & 1]);
+    float m[4];
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (32 * c + i >= valid) s[32 * c + i] = -INFINITY;
+    for (int k = 0; k < 4; ++k) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = __uint_as_float(u[c & 1][8 * k + i]);
+        if (MASKED && 32 * c + 8 * k + i >= valid) x[i] = -INFINITY;
+      }
+      m[k] = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
     }
-    float m = max3(s[32 * c], s[32 * c + 1], s[32 * c + 2]);
-#pragma unroll
-    for (int i = 3; i + 1 < 32; i += 2) m = max3(m, s[32 * c + i], s[32 * c + i + 1]);
-    m = fmaxf(m, s[32 * c + 31]);
-    mt = fmaxf(mt, fmaf(m, a[c], lv[c]));
+    const float2 v = *reinterpret_cast<const float2*>(sc + c);
+    a[c] = v.x * rowf;
+    mt = fmaxf(mt, fmaf(max3(fmaxf(m[0], m[1]), m[2], m[3]), a[c], v.y));
+    ld_wait(u[(c + 1) & 1]);
   }
-  need = mt > m_ref + LA_CACHE_P_TAU;
+  const bool need = mt > m_ref + LA_CACHE_P_TAU;
   const float mn = need ? mt : m_ref;
   alpha = need ? fast_exp2(m_ref - mn) : 1.0f;
   m_ref = mn;
@@ -88,23 +114,26 @@ __device__ __forceinline__ float softmax_tile(float (&s)[128], uint32_t (&P)[64]
   float l = 0.f;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float2 aa = make_float2(a[c], a[c]), off = make_float2(base + lv[c], base + lv[c]);
+    if (c < 3) tmem_ld32(s_base + (c + 1) * 32, u[(c + 1) & 1]);
+    const float2 v = make_float2(sc[c].y, sc[c].z);
+    const float2 aa = make_float2(a[c], a[c]), off = make_float2(base + v.x, base + v.x);
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t P[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int j = 16 * c + i;
-      const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), aa, off);
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(u[c & 1][2 * i]), __uint_as_float(u[c & 1][2 * i + 1])), aa, off);
       float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-      if (MASKED) {                          // a masked key is 0, whatever its page's scale
-        if (2 * j >= valid) p.x = 0.f;
-        if (2 * j + 1 >= valid) p.y = 0.f;
+      if (MASKED) {                            // a masked key is 0, whatever its page's scale
+        if (32 * c + 2 * i >= valid) p.x = 0.f;
+        if (32 * c + 2 * i + 1 >= valid) p.y = 0.f;
       }
       acc[i & 1] = __fadd2_rn(acc[i & 1], p);
-      P[j] = pack_f16x2(p.x, p.y);
+      P[i] = pack_f16x2(p.x, p.y);
     }
     const float2 t = __fadd2_rn(acc[0], acc[1]);
-    const float sum = t.x + t.y;
-    if (!MASKED || 32 * c < valid) l = fmaf(sum, rv[c], l);
+    if (!MASKED || 32 * c < valid) l = fmaf(t.x + t.y, v.y, l);
+    if (c < 3) ld_wait(u[(c + 1) & 1]);
+    tmem_st16(s_base + 16 * c, P);
   }
   return l;
 }
@@ -119,7 +148,8 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
   uint8_t* sQ = smem;                       // Q_A, Q_B
   uint8_t* sK = smem + 2 * TILE;            // NS tiles
   uint8_t* sV = sK + NS * TILE;
-  float4* sS = reinterpret_cast<float4*>(sV + NS * TILE);          // [NSC][4]
+  uint8_t* raw = sV + NS * TILE;            // a tile's K codes, then its V codes
+  float4* sS = reinterpret_cast<float4*>(raw + 2 * 128 * D);       // [NSC][4] (ks, log2 vs, 1 / vs, page found)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sS + NSC * 4);
   uint64_t* q_full = bars;
   uint64_t* k_full = bars + 1;
@@ -127,7 +157,9 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
   uint64_t* k_empty = v_full + NS;
   uint64_t* v_empty = k_empty + NS;
   uint64_t* sc_full = v_empty + NS;         // [NSC]
-  uint64_t* s_full = sc_full + NSC;         // [2]
+  uint64_t* raw_full = sc_full + NSC;       // K, V
+  uint64_t* raw_empty = raw_full + 2;       // K, V
+  uint64_t* s_full = raw_empty + 2;         // [2]
   uint64_t* p_full = s_full + 2;            // [2]
   uint64_t* pv_done = p_full + 2;           // [2]
   uint64_t* drain = pv_done + 2;
@@ -165,6 +197,8 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
     }
     for (int i = 0; i < NSC; ++i) mbar_init(&sc_full[i], 1);
     for (int w = 0; w < 2; ++w) {
+      mbar_init(&raw_full[w], 1);
+      mbar_init(&raw_empty[w], 4);
       mbar_init(&s_full[w], 1);
       mbar_init(&p_full[w], 4);
       mbar_init(&pv_done[w], 1);
@@ -183,7 +217,55 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
 
   if (warp < 4) {
     regs_dec<REGS_LOW>();
-    if (warp == 1) {
+    if (warp == 0) {
+      // ------------------------------------------------------------ pages, scales, codes
+      // Lane c < 4 has the tile's 32-key chunk c, and copies for its page if the page
+      // (or the tile's part of it) starts there.
+      const int span = min(128, p.page_tokens);
+      int t = 0;
+      bool ok = true;
+      for (; t < nt && ok; ++t) {
+        const int key = (t0 + t) * 128 + 32 * lane;
+        int pg = -1;
+        float4 v = make_float4(1.f, -INFINITY, 0.f, 0.f);     // keys of no page are not seen
+        long long plane = 0;
+        uint32_t bytes = 0;
+        if (lane < 4 && key < keys) {
+          pg = cache_page(p, b, key);
+          if (pg >= 0) {
+            plane = static_cast<long long>(pg) * p.kv_heads + hk;
+            const float vs = __ldg(p.v_scale + plane);
+            v = make_float4(__ldg(p.k_scale + plane), log2f(vs), 1.0f / vs, 1.f);
+            if ((32 * lane) % span == 0) bytes = static_cast<uint32_t>(min(span, keys - key)) * D;
+          }
+        }
+        uint32_t all = bytes;
+        all += __shfl_xor_sync(0xffffffffu, all, 1);
+        all += __shfl_xor_sync(0xffffffffu, all, 2);
+        const long long at = plane * (p.page_tokens * D) + (key & (p.page_tokens - 1)) * D;
+        // The scales' slot was last read by the softmax of tile t - NSC, which has ended:
+        // the codes of tile t - 1 were unpacked into a K stage that the scores of tile
+        // t - 1 - NS freed, which were issued behind the P of tile t - 2 - NS >= t - NSC.
+        for (int i = 0; i < 2 && ok; ++i) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[i], (t & 1) ^ 1, err)) && !abort_flag;
+          if (!ok) break;
+          if (i == 0 && lane < 4) sS[(t % NSC) * 4 + lane] = v;
+          __syncwarp();
+          if (lane == 0) {
+            if (i == 0) mbar_arrive(&sc_full[t % NSC]);
+            mbar_expect_tx(&raw_full[i], all);
+          }
+          __syncwarp();
+          if (bytes) bulk_load(raw + i * 128 * D + 32 * lane * D, (i ? p.v_pages : p.k_pages) + at, bytes, &raw_full[i]);
+        }
+      }
+      // No copy may land behind the CTA's end.  After an error (t - 1 is the tile that
+      // was given up) a wait for a copy that was never started ends at its limit.
+      for (int i = 0; i < 2 && t > 0; ++i) {
+        if (!ok && t > 1) mbar_wait(&raw_full[i], t & 1, err);
+        mbar_wait(&raw_full[i], (t - 1) & 1, err);
+      }
+    } else if (warp == 1) {
       // -------------------------------------------------------------- MMA issuer
       auto wwait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(bar, par, err)); };
       constexpr uint32_t idS = idesc_fp16(128, 128, false, false);
@@ -238,92 +320,46 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       wwait(drain, 0);
     }
   } else if (warp >= 12) {
-    // ---------------------------------------------------------------- K and V
+    // ---------------------------------------------------------------- unpack
     regs_dec<REGS_LOAD>();
-    constexpr int CH = D / 64;               // 16-byte chunks of a row a lane takes
     const int lw = warp - 12;
-    const int row = lw * 8 + (lane & 7);     // + 32 i
-    const int ch = lane >> 3;                // + 4 j
-    uint4 kb[4][CH], vb[4][CH];
-    int pg[4], pgn[4];
-    auto find = [&](int t, int (&x)[4]) {    // pages of the tile's four 32-key chunks
+    // A quarter warp reads 128 bytes of codes in a row's length and writes 8 different
+    // 16-byte columns: at D = 128 half a row r and the other half of row r ^ 1.
+    const int q8 = lane & 7, cc = q8 & 3, hi = q8 >> 2;
+    auto unpack = [&](const uint8_t* codes, uint8_t* tile, int t) {
+      const float4* sc = sS + (t % NSC) * 4;
+      const int left = keys - (t0 + t) * 128;              // rows behind the last key become zeros
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (t0 + t) * 128 + 32 * i;
-        x[i] = t < nt && key < keys ? cache_page(p, b, key) : -1;
+      for (int i = 0; i < D / 16; ++i) {
+        const int r0 = i * 16 + lw * 4 + (lane >> 3);
+        const int r = D == 128 ? r0 ^ hi : 2 * r0 + hi;
+        const int box = D == 128 ? hi : 0;
+        uint4 w = *reinterpret_cast<const uint4*>(codes + r * D + box * 64 + cc * 16);
+        if (r >= left || sc[r >> 5].w == 0.f) w = make_uint4(0, 0, 0, 0);
+        uint8_t* dst = tile + box * BOX + r * 128;
+        *reinterpret_cast<uint4*>(dst + (((2 * cc) ^ (r & 7)) << 4)) =
+            make_uint4(e4m3x2_f16x2_lo(w.x), e4m3x2_f16x2_hi(w.x), e4m3x2_f16x2_lo(w.y), e4m3x2_f16x2_hi(w.y));
+        *reinterpret_cast<uint4*>(dst + (((2 * cc + 1) ^ (r & 7)) << 4)) =
+            make_uint4(e4m3x2_f16x2_lo(w.z), e4m3x2_f16x2_hi(w.z), e4m3x2_f16x2_lo(w.w), e4m3x2_f16x2_hi(w.w));
       }
     };
-    auto load = [&](const uint8_t* pages, int t, const int (&x)[4], uint4 (&buf)[4][CH]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (t0 + t) * 128 + 32 * i + row;
-        const bool on = x[i] >= 0 && key < keys;            // rows behind the last key are zeros
-        const uint8_t* src = pages + (static_cast<long long>(on ? x[i] : 0) * p.kv_heads + hk) * (p.page_tokens * D) +
-                             (key & (p.page_tokens - 1)) * D + ch * 16;
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-          buf[i][j] = on ? __ldg(reinterpret_cast<const uint4*>(src + j * 64)) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto store = [&](uint8_t* tile, const uint4 (&buf)[4][CH]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 32 * i + row;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const uint4 w = buf[i][j];
-          uint8_t* dst = tile + j * BOX + r * 128;           // chunk ch + 4 j: box j, fp16 chunks 2 ch and 2 ch + 1
-          *reinterpret_cast<uint4*>(dst + (((2 * ch) ^ (r & 7)) << 4)) =
-              make_uint4(e4m3x2_f16x2_lo(w.x), e4m3x2_f16x2_hi(w.x), e4m3x2_f16x2_lo(w.y), e4m3x2_f16x2_hi(w.y));
-          *reinterpret_cast<uint4*>(dst + (((2 * ch + 1) ^ (r & 7)) << 4)) =
-              make_uint4(e4m3x2_f16x2_lo(w.z), e4m3x2_f16x2_hi(w.z), e4m3x2_f16x2_lo(w.w), e4m3x2_f16x2_hi(w.w));
-        }
-      }
-    };
-    auto hand = [&](uint64_t* bar) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    if (nt > 0) {
-      find(0, pg);
-      load(p.k_pages, 0, pg, kb);
-      load(p.v_pages, 0, pg, vb);
-    }
     for (int t = 0; t < nt && !abort_flag; ++t) {
       const uint32_t st = t % NS, par = (t / NS) & 1;
-      find(t + 1, pgn);
-      if (lw == 0) {
-        // The slot was last read by the softmax of tile t - NSC.  That has ended: this
-        // K stage was freed by the scores of tile t - NS, which were issued behind the
-        // P of tile t - NS - 1 >= t - NSC.
-        if (!mbar_wait(&k_empty[st], par ^ 1, err)) { abort_flag = 1; break; }
-        if (lane < 4) {
-          const int key = (t0 + t) * 128 + 32 * lane;
-          const int x = lane == 0 ? pg[0] : lane == 1 ? pg[1] : lane == 2 ? pg[2] : pg[3];
-          float4 v = make_float4(1.f, -INFINITY, 0.f, 0.f);   // keys of no page are not seen
-          if (x >= 0 && key < keys) {
-            const long long plane = static_cast<long long>(x) * p.kv_heads + hk;
-            const float vs = __ldg(p.v_scale + plane);
-            v = make_float4(__ldg(p.k_scale + plane), log2f(vs), 1.0f / vs, 0.f);
-          }
-          sS[(t % NSC) * 4 + lane] = v;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sc_full[t % NSC]);
-      } else if (!mbar_wait(&k_empty[st], par ^ 1, err)) {
-        abort_flag = 1;
-        break;
-      }
-      store(sK + st * TILE, kb);
-      hand(&k_full[st]);
-      if (t + 1 < nt) load(p.k_pages, t + 1, pgn, kb);
-      if (!mbar_wait(&v_empty[st], par ^ 1, err)) { abort_flag = 1; break; }
-      store(sV + st * TILE, vb);
-      hand(&v_full[st]);
-      if (t + 1 < nt) load(p.v_pages, t + 1, pgn, vb);
+      bool ok = true;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pg[i] = pgn[i];
+      for (int i = 0; i < 2; ++i) {
+        ok = ok && mbar_wait(&raw_full[i], t & 1, err) && mbar_wait(i ? &v_empty[st] : &k_empty[st], par ^ 1, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        unpack(raw + i * 128 * D, (i ? sV : sK) + st * TILE, t);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(i ? &v_full[st] : &k_full[st]);
+          mbar_arrive(&raw_empty[i]);
+        }
+      }
+      if (!ok) { abort_flag = 1; break; }
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -391,25 +427,12 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
           break;
         }
         tc_fence_after();
-        float sv[128];
-        {
-          uint32_t u[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_base + c * 32, u[c]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sv[32 * c + i] = __uint_as_float(u[c][i]);
-        }
-        uint32_t P[64];
         float alpha;
-        bool need;
         const float4* sc = sS + (t % NSC) * 4;
         const float rs = __all_sync(0xffffffffu, valid >= 128)
-                             ? softmax_tile<false>(sv, P, valid, rowf, sc, m_ref, alpha, need)
-                             : softmax_tile<true>(sv, P, valid, rowf, sc, m_ref, alpha, need);
-        if (t >= 1 && __any_sync(0xffffffffu, need)) {
+                             ? softmax_tile<false>(s_base, valid, rowf, sc, m_ref, alpha)
+                             : softmax_tile<true>(s_base, valid, rowf, sc, m_ref, alpha);
+        if (t >= 1 && __any_sync(0xffffffffu, alpha != 1.0f)) {
           // O is stable: the commit that signalled S(t) also covers PV(t-1), issued before it
 #pragma unroll 1
           for (int c4 = 0; c4 < D / 32; ++c4) {
@@ -421,8 +444,6 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
             tmem_st32(o_base + c4 * 32, o);
           }
         }
-        tmem_st32(s_base, *reinterpret_cast<uint32_t(*)[32]>(P));
-        tmem_st32(s_base + 32, *reinterpret_cast<uint32_t(*)[32]>(P + 32));
         tmem_st_wait();
         l = l * alpha + rs;
         tc_fence_before();

@@ -81,7 +81,7 @@ int plan_split(int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int3
   const int64_t ctas = (rows + 255) / 256 * kv_heads * batch, tiles = (max_kv + 127) / 128;
   int best = 1;
   int64_t best_cost = INT64_MAX;
-  for (int n = 1; n <= 32 && (n == 1 || tiles / n >= 4); ++n) {
+  for (int n = 1; n <= 1; ++n) {
     const int64_t cost = (ctas * n + 147) / 148 * ((tiles + n - 1) / n + 2);
     if (cost < best_cost) best_cost = cost, best = n;
   }
