@@ -4,7 +4,10 @@
 // One CTA takes one page of one sequence, for K or for V, and walks over heads:
 // it holds the page's new tokens in registers (fp32, after the rotation), reduces
 // their largest magnitude over the CTA, picks the scale and writes the codes, so
-// every new element is read once and every code written once.  Bound: HBM.
+// every new element is read once and every code written once.  The next heads'
+// elements are on their way meanwhile (cp.async to a ring in shared memory, of which
+// each thread reads back what it copied, so nothing waits for another thread but the
+// reduction).  Bound: HBM.
 //
 // Scale: 2^k, the smallest with 448 * 2^k >= amax (k >= -64), read off amax's own
 // exponent and mantissa, so no rounding decides it.  A page that already holds
@@ -13,13 +16,13 @@
 // to e4m3 again: exact but for results below e4m3's normal range.  A magnitude
 // that is not finite makes the scale NaN, which marks the page's head until its
 // first token is written again.
+#include <algorithm>
+
 #include "kernels.h"
 #include "rotary.cuh"
 #include "sm100.cuh"
 
 namespace {
-
-constexpr int THREADS = 256;
 
 // Smallest 2^k >= amax / 448 for the bits of amax >= 0: 448 = 1.75 * 2^8.
 __device__ __forceinline__ float page_scale(uint32_t amax_bits) {
@@ -35,15 +38,36 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
+__device__ __forceinline__ float max_nan3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Vectors of the input that a thread holds for one head, and the ring's stages.
+template <typename T, int D, int PAGE> struct Ring {
+  static constexpr int ALL = PAGE * D / 16;                  // threads that hold a page's head at 16 elements each
+  static constexpr int THREADS = ALL < 512 ? ALL : 512;
+  static constexpr int NP = ALL / THREADS;
+  static constexpr int PER = 16 / Vec16<T>::N;               // 16-byte vectors of 16 elements
+  static constexpr int STAGE = NP * PER * THREADS * 16;
+  static constexpr int STAGES = STAGE <= 16384 ? 4 : STAGE <= 32768 ? 3 : 2;
+};
+
 // A thread owns 8 pairs of one token a pass: pairs 8u .. 8u+7 of its row, D/16
 // threads a row.  VEC: the pairs' elements are 16-byte vectors of the input and 16
 // (or twice 8) consecutive codes.
 template <typename T, int D, int PAGE, bool VEC>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__((Ring<T, D, PAGE>::THREADS))
 k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constant__ RotaryTable tab) {
+  using R = Ring<T, D, PAGE>;
+  constexpr int THREADS = R::THREADS, NP = R::NP;
   constexpr int TPR = D / 16;                       // threads a row
   constexpr int ROWS = THREADS / TPR;               // rows a pass
-  constexpr int NP = (PAGE + ROWS - 1) / ROWS;
   constexpr int N = Vec16<T>::N;
   const int b = blockIdx.x / p.pages_per_seq, at = blockIdx.x % p.pages_per_seq;
   const bool is_v = blockIdx.z != 0;
@@ -71,48 +95,79 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
   }
   const long long tok0 = c0 + (start - old_len);    // first new token of the page
 
+  const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.heads);
+  const T* x = static_cast<const T*>(is_v ? p.v : p.k);
+  const long long st = is_v ? p.v_st : p.k_st, sh = is_v ? p.v_sh : p.k_sh;
+  const bool half = tab.half && !is_v && 8 * u < tab.n;   // this thread's pairs lie n apart
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  uint4* ring = reinterpret_cast<uint4*>(ring_raw);
+  auto fetch = [&](int h) {
+    if constexpr (VEC) {
+      if (h < h1) {
+        uint4* to = ring + (h - h0) % R::STAGES * (R::STAGE / 16) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int r = row + i * ROWS;
+          if (r < cnt) {
+            const T* xr = x + (tok0 + r) * st + h * sh;
+            const T* lo = half ? xr + 8 * u : xr + 16 * u;
+            const T* hi = half ? xr + tab.n + 8 * u : xr + 16 * u + 8;
+#pragma unroll
+            for (int w = 0; w < 8 / N; ++w) {
+              cp_async16(to + (i * R::PER + w) * THREADS, lo + w * N);
+              cp_async16(to + (i * R::PER + 8 / N + w) * THREADS, hi + w * N);
+            }
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  for (int i = 0; i < R::STAGES - 1; ++i) fetch(h0 + i);
+
   float2 cs[NP][8];
   const bool rotate = !is_v && tab.n > 0;
   if (rotate) {
+    __shared__ PairTable pairs;
+    pairs.fill(tab);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = row + i * ROWS;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        cs[i][k] = r < cnt && 8 * u + k < tab.n ? pair_cos_sin(tab, 8 * u + k, p.pos + (tok0 + r) * tab.naxes) : make_float2(1.f, 0.f);
+        cs[i][k] = r < cnt && 8 * u + k < tab.n ? pairs.cos_sin(8 * u + k, p.pos + (tok0 + r) * tab.naxes, false) : make_float2(1.f, 0.f);
     }
   }
   __shared__ uint32_t red[2][THREADS / 32];
-  const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.heads);
-  const T* x = static_cast<const T*>(is_v ? p.v : p.k);
-  const long long st = is_v ? p.v_st : p.k_st, sh = is_v ? p.v_sh : p.k_sh;
   float* scales = is_v ? p.v_scale : p.k_scale;
   uint8_t* pages = is_v ? p.v_pages : p.k_pages;
-  const bool half = tab.half && !is_v && 8 * u < tab.n;   // this thread's pairs lie n apart
 
   for (int h = h0; h < h1; ++h) {
+    if constexpr (VEC) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(R::STAGES - 2) : "memory");
+      fetch(h + R::STAGES - 1);                     // into the stage that this thread read a head ago
+    }
+    const uint4* from = ring + (h - h0) % R::STAGES * (R::STAGE / 16) + threadIdx.x;
     float f[NP][16];                                // pair k of the 8: f[2k], f[2k+1]
-    uint32_t amax = 0;
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = row + i * ROWS;
       if (r < cnt) {
-        const T* xr = x + (tok0 + r) * st + h * sh;
         if constexpr (VEC) {
           float a[16];
-          const T* lo = half ? xr + 8 * u : xr + 16 * u;
-          const T* hi = half ? xr + tab.n + 8 * u : xr + 16 * u + 8;
 #pragma unroll
-          for (int w = 0; w < 8 / N; ++w) {
-            Vec16<T>::unpack(*reinterpret_cast<const uint4*>(lo + w * N), a + w * N);
-            Vec16<T>::unpack(*reinterpret_cast<const uint4*>(hi + w * N), a + 8 + w * N);
-          }
+          for (int w = 0; w < R::PER; ++w) Vec16<T>::unpack(from[(i * R::PER + w) * THREADS], a + w * N);
+          if (half) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            f[i][2 * k] = half ? a[k] : a[2 * k];
-            f[i][2 * k + 1] = half ? a[8 + k] : a[2 * k + 1];
+            for (int k = 0; k < 16; ++k) f[i][k] = a[k / 2 + (k & 1) * 8];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[i][k] = a[k];
           }
         } else {
+          const T* xr = x + (tok0 + r) * st + h * sh;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int2 e = is_v ? make_int2(16 * u + 2 * k, 16 * u + 2 * k + 1) : pair_elems(tab, 8 * u + k);
@@ -131,13 +186,13 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
           }
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) amax = max(amax, __float_as_uint(f[i][k]) & 0x7fffffffu);   // NaN > inf > finite
+        for (int k = 0; k < 8; ++k) top = max_nan3(top, fabsf(f[i][2 * k]), fabsf(f[i][2 * k + 1]));
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k) f[i][k] = 0.f;
       }
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // bits: NaN > inf > finite
     uint32_t* rd = red[(h - h0) & 1];
     if (threadIdx.x % 32 == 0) rd[threadIdx.x / 32] = amax;
     float* sc = scales + static_cast<long long>(pg) * p.heads + h;
@@ -171,17 +226,21 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
           for (int k = 0; k < 16; ++k) f[i][k] = 0.f;
         }
         if constexpr (VEC) {
-          float a[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) a[k] = (half ? f[i][k < 8 ? 2 * k : 2 * k - 15] : f[i][k]) * inv;
           uint32_t w[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            w[q] = pack_e4m3x4(make_float2(a[4 * q], a[4 * q + 1]), make_float2(a[4 * q + 2], a[4 * q + 3]));
           if (half) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float* a = f[i] + 8 * (q & 1) + (q >> 1);
+              w[q] = pack_e4m3x4(make_float2(a[0] * inv, a[2] * inv), make_float2(a[4] * inv, a[6] * inv));
+            }
             *reinterpret_cast<uint2*>(cr + 8 * u) = make_uint2(w[0], w[1]);
             *reinterpret_cast<uint2*>(cr + tab.n + 8 * u) = make_uint2(w[2], w[3]);
           } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float* a = f[i] + 4 * q;
+              w[q] = pack_e4m3x4(make_float2(a[0] * inv, a[1] * inv), make_float2(a[2] * inv, a[3] * inv));
+            }
             *reinterpret_cast<uint4*>(cr + 16 * u) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
@@ -213,8 +272,17 @@ cudaError_t launch(CacheAppendParams p, const RotaryTable& tab, int num_sms, cud
   long long hpc = gx * 2 * p.heads / (num_sms * 4LL);
   p.heads_per_cta = static_cast<int>(hpc < 1 ? 1 : (hpc > 8 ? 8 : hpc));
   dim3 grid(static_cast<unsigned>(gx), ceil_div_i(p.heads, p.heads_per_cta), 2);
-  if (vec) k_cache_append<T, D, PAGE, true><<<grid, THREADS, 0, st>>>(p, tab);
-  else k_cache_append<T, D, PAGE, false><<<grid, THREADS, 0, st>>>(p, tab);
+  using R = Ring<T, D, PAGE>;
+  if (!vec) {
+    k_cache_append<T, D, PAGE, false><<<grid, R::THREADS, 0, st>>>(p, tab);
+    return cudaGetLastError();
+  }
+  // As much of the ring as the CTA's heads fill.
+  const int smem = R::STAGE * std::min(R::STAGES, p.heads_per_cta);
+  auto kern = k_cache_append<T, D, PAGE, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::STAGE * R::STAGES);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, R::THREADS, smem, st>>>(p, tab);
   return cudaGetLastError();
 }
 

@@ -5,24 +5,33 @@
 // (the inverse, which is also the gradient, turns by -a).  Bound: HBM, every
 // element read and written once.  A thread owns one run of pairs of one token and
 // walks over heads, so a sine and cosine pair is computed once for all the heads
-// that the thread visits.
+// that the thread visits; it reads BATCH heads before it writes the first of them,
+// which keeps that many 16-byte loads under way (in place, too: the elements are its
+// own).
 #include "kernels.h"
 #include "rotary.cuh"
 
 namespace {
 
-// VEC: 16-byte accesses.  Pairs a thread owns: interleaved, the N/2 pairs of one
+constexpr int BATCH = 4;
+
+// VEC: 16-byte accesses (HALF: tab.half).  Pairs a thread owns: interleaved, the N/2 pairs of one
 // 16-byte vector; halves, the N pairs of the vectors at j and n + j; passed-through
 // elements, N/2 "pairs" of one vector.  Not VEC: one pair.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool HALF>
 __global__ void __launch_bounds__(256)
 k_rope_axes(const __grid_constant__ RopeAxesParams p, const __grid_constant__ RotaryTable tab) {
   constexpr int N = Vec16<T>::N;
-  const int units = p.units;
-  const long long i = blockIdx.x * 256LL + threadIdx.x;
-  const long long t = i / units;
+  __shared__ PairTable pairs;
+  pairs.fill(tab);
+  __syncthreads();
+  // A CTA's 256 units start at token t0, unit u0 of it.
+  const long long i0 = blockIdx.x * 256LL;
+  const long long t0 = i0 / p.units;
+  const unsigned at = static_cast<unsigned>(i0 - t0 * p.units) + threadIdx.x;
+  const long long t = t0 + at / static_cast<unsigned>(p.units);
   if (t >= p.tokens) return;
-  const int u = static_cast<int>(i - t * units);
+  const int u = static_cast<int>(at % static_cast<unsigned>(p.units));
   const int h0 = blockIdx.y * p.heads_per_thread;
   const int h1 = min(h0 + p.heads_per_thread, p.heads);
   const int* pos = p.pos + t * tab.naxes;
@@ -36,46 +45,50 @@ k_rope_axes(const __grid_constant__ RopeAxesParams p, const __grid_constant__ Ro
         *reinterpret_cast<uint4*>(y + h * p.o_sh + e) = *reinterpret_cast<const uint4*>(x + h * p.x_sh + e);
       return;
     }
-    if (tab.half) {
-      float2 cs[N];
+    const int lo = u * N, hi = tab.half ? tab.n + u * N : 0;
+    float2 cs[N];
+    for (int h = h0; h < h1; h += BATCH) {
+      uint4 a[BATCH], b[BATCH];
 #pragma unroll
-      for (int k = 0; k < N; ++k) cs[k] = pair_cos_sin(tab, u * N + k, pos);
-#pragma unroll 2
-      for (int h = h0; h < h1; ++h) {
-        float a[N], b[N];
-        Vec16<T>::unpack(*reinterpret_cast<const uint4*>(x + h * p.x_sh + u * N), a);
-        Vec16<T>::unpack(*reinterpret_cast<const uint4*>(x + h * p.x_sh + tab.n + u * N), b);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const float v = a[k];
-          a[k] = v * cs[k].x - b[k] * cs[k].y;
-          b[k] = v * cs[k].y + b[k] * cs[k].x;
-        }
-        *reinterpret_cast<uint4*>(y + h * p.o_sh + u * N) = Vec16<T>::pack(a);
-        *reinterpret_cast<uint4*>(y + h * p.o_sh + tab.n + u * N) = Vec16<T>::pack(b);
+      for (int k = 0; k < BATCH; ++k) {
+        if (h + k >= h1) continue;
+        a[k] = *reinterpret_cast<const uint4*>(x + (h + k) * p.x_sh + lo);
+        if (HALF) b[k] = *reinterpret_cast<const uint4*>(x + (h + k) * p.x_sh + hi);
       }
-    } else {
-      float2 cs[N / 2];
+      if (h == h0) {                            // behind the first loads
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) cs[k] = pair_cos_sin(tab, u * (N / 2) + k, pos);
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h) {
-        float a[N];
-        Vec16<T>::unpack(*reinterpret_cast<const uint4*>(x + h * p.x_sh + u * N), a);
+        for (int k = 0; k < (HALF ? N : N / 2); ++k) cs[k] = pairs.cos_sin(u * (HALF ? N : N / 2) + k, pos, tab.inverse);
+      }
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) {
-          const float v = a[2 * k], w = a[2 * k + 1];
-          a[2 * k] = v * cs[k].x - w * cs[k].y;
-          a[2 * k + 1] = v * cs[k].y + w * cs[k].x;
+      for (int k = 0; k < BATCH; ++k) {
+        if (h + k >= h1) continue;
+        float f[N], g[N];
+        Vec16<T>::unpack(a[k], f);
+        if constexpr (HALF) {
+          Vec16<T>::unpack(b[k], g);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float v = f[e];
+            f[e] = v * cs[e].x - g[e] * cs[e].y;
+            g[e] = v * cs[e].y + g[e] * cs[e].x;
+          }
+          *reinterpret_cast<uint4*>(y + (h + k) * p.o_sh + hi) = Vec16<T>::pack(g);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) {
+            const float v = f[2 * e], w = f[2 * e + 1];
+            f[2 * e] = v * cs[e].x - w * cs[e].y;
+            f[2 * e + 1] = v * cs[e].y + w * cs[e].x;
+          }
         }
-        *reinterpret_cast<uint4*>(y + h * p.o_sh + u * N) = Vec16<T>::pack(a);
+        *reinterpret_cast<uint4*>(y + (h + k) * p.o_sh + lo) = Vec16<T>::pack(f);
       }
     }
   } else {
     const int2 e = pair_elems(tab, u);
     const bool turn = u < tab.n;
     const bool two = e.y < p.d;                 // an odd d passes one last element through
-    const float2 cs = turn ? pair_cos_sin(tab, u, pos) : make_float2(1.f, 0.f);
+    const float2 cs = turn ? pairs.cos_sin(u, pos, tab.inverse) : make_float2(1.f, 0.f);
     for (int h = h0; h < h1; ++h) {
       const T* xr = x + h * p.x_sh;
       T* yr = y + h * p.o_sh;
@@ -108,8 +121,9 @@ cudaError_t launch(RopeAxesParams p, const RotaryTable& tab, int num_sms, cudaSt
   const long long gx = (per_head + 255) / 256;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;
   dim3 grid(static_cast<unsigned>(gx), ceil_div_i(p.heads, p.heads_per_thread));
-  if (vec) k_rope_axes<T, true><<<grid, 256, 0, st>>>(p, tab);
-  else k_rope_axes<T, false><<<grid, 256, 0, st>>>(p, tab);
+  if (!vec) k_rope_axes<T, false, false><<<grid, 256, 0, st>>>(p, tab);
+  else if (tab.half) k_rope_axes<T, true, true><<<grid, 256, 0, st>>>(p, tab);
+  else k_rope_axes<T, true, false><<<grid, 256, 0, st>>>(p, tab);
   return cudaGetLastError();
 }
 

@@ -3,9 +3,11 @@
 // Pair j (of n) turns by pos[axis(j)] * omega_j.  The angle is kept in turns as a
 // 64-bit fixed-point fraction: omega_j / (2 pi) * 2^64 is rounded once on the host
 // and the product with the (signed) position wraps modulo 2^64, which is exactly
-// "modulo one turn".  Its error is |pos| * 2^-65 turns for every position an int32
-// holds, where pos * omega in fp32 would lose 2^-24 * pos * omega radians (6e-3 at
-// position 1e5).  The top 32 bits, as a signed fraction of half turns, go to sincospif.
+// "modulo one turn".  Its error is |pos| * 2^-62 turns at most, for every position an
+// int32 holds, where pos * omega in fp32 would lose 2^-24 * pos * omega radians (6e-3
+// at position 1e5).  Its top 32 bits, as an integer, give the quadrant and the signed
+// rest within an eighth of a turn exactly; the rest goes to fp32 once and into the
+// Taylor series of sine and cosine about 0 (next terms at pi/4: 3e-9 and 4e-10).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -19,12 +21,41 @@ __device__ __forceinline__ int2 pair_elems(const RotaryTable& t, int j) {
   return make_int2(2 * j, 2 * j + 1);
 }
 
-__device__ __forceinline__ float2 pair_cos_sin(const RotaryTable& t, int j, const int* pos) {
-  const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos[t.axis[j]])) * t.turn[j];
-  float s, c;
-  sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
-  return make_float2(c, t.inverse ? -s : s);
+__device__ __forceinline__ float2 turn_cos_sin(uint32_t turn) {   // turn: of 2^32
+  const uint32_t q = (turn + 0x20000000u) >> 30;
+  const float u = static_cast<float>(static_cast<int>(turn - (q << 30))) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float w = u * u;
+  float s = fmaf(w, 2.7557319223985893e-6f, -1.9841269841269841e-4f);   // 1/9!, -1/7!
+  s = fmaf(s, w, 8.3333333333333333e-3f);                                // 1/5!
+  s = fmaf(s, w, -1.6666666666666667e-1f);                               // -1/3!
+  s = fmaf(s * w, u, u);
+  float c = fmaf(w, -2.7557319223985888e-7f, 2.4801587301587302e-5f);   // -1/10!, 1/8!
+  c = fmaf(c, w, -1.3888888888888889e-3f);                               // -1/6!
+  c = fmaf(c, w, 4.1666666666666664e-2f);                                // 1/4!
+  c = fmaf(c, w, -0.5f);
+  c = fmaf(c, w, 1.0f);
+  const float a = q & 1 ? s : c, b = q & 1 ? c : s;                      // |cos|, |sin| up to their signs
+  return make_float2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
 }
+
+// The table's pairs in shared memory: lanes of a warp ask for different pairs, which the
+// constant bank that holds the launch's arguments would serve one after the other.
+// Filled by all threads of the CTA; they meet before they use it.
+struct PairTable {
+  unsigned long long turn[LA_ROPE_MAX_PAIRS];
+  unsigned char axis[LA_ROPE_MAX_PAIRS];
+  __device__ __forceinline__ void fill(const RotaryTable& t) {
+    for (int j = threadIdx.x; j < t.n; j += blockDim.x) {
+      turn[j] = t.turn[j];
+      axis[j] = t.axis[j];
+    }
+  }
+  __device__ __forceinline__ float2 cos_sin(int j, const int* pos, bool inverse) const {
+    const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos[axis[j]])) * turn[j];
+    const float2 v = turn_cos_sin(static_cast<uint32_t>(ph >> 32));
+    return make_float2(v.x, inverse ? -v.y : v.y);
+  }
+};
 
 template <typename T> struct Vec16;             // 16 bytes of T as fp32 values
 template <> struct Vec16<float> {

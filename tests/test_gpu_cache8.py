@@ -2,9 +2,10 @@
 definitions in 64 bits (oracle/cache8.py) on the same inputs.
 
 Tolerances (u = 2^-24, eps_t the type's epsilon):
-  rotation   an angle is a fraction of a turn exact to 2^-32 and then one fp32 conversion below 1 (2^-25 half turns,
-             9.4e-8 rad); sincospif is within 2 ulp (2.4e-7 at most); the two products and the sum add 3 u: together
-             TURN * (|x0| + |x1|) with TURN = 9.4e-8 + 2.4e-7 + 1.8e-7 = 5.2e-7, plus half a step of the output.
+  rotation   an angle is a fraction of a turn exact to 2^-32 (1.5e-9 rad); its rest within an eighth of a turn goes to
+             fp32 and is scaled there (3 u of at most pi/4: 1.4e-7 rad), the series and its evaluation add 2 u and 3e-9;
+             the two products and the sum add 3 u: together at most TURN * (|x0| + |x1|) with TURN = 5.2e-7, plus half a
+             step of the output.
   append     V's scales and codes are integer decisions on the input: equal.  A rotated K lies within the rotation's
              bound of the exact one: its value is off by half an e4m3 step plus that, and its scale is the exact one's
              unless the page's largest magnitude is within the bound of 448 * 2^e.
