@@ -61,7 +61,8 @@ template <typename T, int D, int PAGE> struct Ring {
 // A thread owns 8 pairs of one token a pass: pairs 8u .. 8u+7 of its row, D/16
 // threads a row.  VEC: the pairs' elements are 16-byte vectors of the input and 16
 // (or twice 8) consecutive codes.
-template <typename T, int D, int PAGE, bool VEC>
+// HALF: tab.half.
+template <typename T, int D, int PAGE, bool VEC, bool HALF>
 __global__ void __launch_bounds__((Ring<T, D, PAGE>::THREADS))
 k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constant__ RotaryTable tab) {
   using R = Ring<T, D, PAGE>;
@@ -98,34 +99,38 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
   const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.heads);
   const T* x = static_cast<const T*>(is_v ? p.v : p.k);
   const long long st = is_v ? p.v_st : p.k_st, sh = is_v ? p.v_sh : p.k_sh;
-  const bool half = tab.half && !is_v && 8 * u < tab.n;   // this thread's pairs lie n apart
+  const bool half = HALF && !is_v && 8 * u < tab.n;   // this thread's pairs lie n apart
   extern __shared__ __align__(16) uint8_t ring_raw[];
   uint4* ring = reinterpret_cast<uint4*>(ring_raw);
+  // Row base of this thread's elements (+ hi for the second vector) at the next head to
+  // fetch, and the stage it goes to.
+  const T* src = x + (tok0 + row) * st + h0 * sh + (half ? 8 * u : 16 * u);
+  const int hi = half ? tab.n : 8;
+  int into = 0;
   auto fetch = [&](int h) {
     if constexpr (VEC) {
       if (h < h1) {
-        uint4* to = ring + (h - h0) % R::STAGES * (R::STAGE / 16) + threadIdx.x;
+        uint4* to = ring + into * (R::STAGE / 16) + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const int r = row + i * ROWS;
-          if (r < cnt) {
-            const T* xr = x + (tok0 + r) * st + h * sh;
-            const T* lo = half ? xr + 8 * u : xr + 16 * u;
-            const T* hi = half ? xr + tab.n + 8 * u : xr + 16 * u + 8;
+          if (row + i * ROWS < cnt) {
+            const T* xr = src + i * ROWS * st;
 #pragma unroll
             for (int w = 0; w < 8 / N; ++w) {
-              cp_async16(to + (i * R::PER + w) * THREADS, lo + w * N);
-              cp_async16(to + (i * R::PER + 8 / N + w) * THREADS, hi + w * N);
+              cp_async16(to + (i * R::PER + w) * THREADS, xr + w * N);
+              cp_async16(to + (i * R::PER + 8 / N + w) * THREADS, xr + hi + w * N);
             }
           }
         }
+        src += sh;
+        into = into + 1 == R::STAGES ? 0 : into + 1;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   };
   for (int i = 0; i < R::STAGES - 1; ++i) fetch(h0 + i);
 
-  float2 cs[NP][8];
+  float2 cs[NP][8];                                 // pairs that are not rotated: (1, 0), exact for finite values
   const bool rotate = !is_v && tab.n > 0;
   if (rotate) {
     __shared__ PairTable pairs;
@@ -139,16 +144,23 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
         cs[i][k] = r < cnt && 8 * u + k < tab.n ? pairs.cos_sin(8 * u + k, p.pos + (tok0 + r) * tab.naxes, false) : make_float2(1.f, 0.f);
     }
   }
-  __shared__ uint32_t red[2][THREADS / 32];
-  float* scales = is_v ? p.v_scale : p.k_scale;
-  uint8_t* pages = is_v ? p.v_pages : p.k_pages;
+  // The CTA's maximum of head h: slot h % 3, cleared two heads before.  A slot is read
+  // behind the barrier of its head and cleared behind the next, which everyone reaches
+  // after reading it.
+  __shared__ uint32_t red[3];
+  if (threadIdx.x < 3) red[threadIdx.x] = 0;
+  __syncthreads();
+  int slot = 0, stage = 0;
+  uint8_t* pl = (is_v ? p.v_pages : p.k_pages) + (static_cast<long long>(pg) * p.heads + h0) * (PAGE * D);
+  float* sc = (is_v ? p.v_scale : p.k_scale) + static_cast<long long>(pg) * p.heads + h0;
 
-  for (int h = h0; h < h1; ++h) {
+  for (int h = h0; h < h1; ++h, ++sc, pl += PAGE * D) {
     if constexpr (VEC) {
       asm volatile("cp.async.wait_group %0;" ::"n"(R::STAGES - 2) : "memory");
       fetch(h + R::STAGES - 1);                     // into the stage that this thread read a head ago
     }
-    const uint4* from = ring + (h - h0) % R::STAGES * (R::STAGE / 16) + threadIdx.x;
+    const uint4* from = ring + stage * (R::STAGE / 16) + threadIdx.x;
+    stage = stage + 1 == R::STAGES ? 0 : stage + 1;
     float f[NP][16];                                // pair k of the 8: f[2k], f[2k+1]
     float top = 0.f;
 #pragma unroll
@@ -178,33 +190,28 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
         if (rotate) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            if (8 * u + k < tab.n) {
-              const float v = f[i][2 * k], w = f[i][2 * k + 1];
-              f[i][2 * k] = v * cs[i][k].x - w * cs[i][k].y;
-              f[i][2 * k + 1] = v * cs[i][k].y + w * cs[i][k].x;
-            }
+            const float v = f[i][2 * k], w = f[i][2 * k + 1];
+            f[i][2 * k] = v * cs[i][k].x - w * cs[i][k].y;
+            f[i][2 * k + 1] = v * cs[i][k].y + w * cs[i][k].x;
           }
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = max_nan3(top, fabsf(f[i][2 * k]), fabsf(f[i][2 * k + 1]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) f[i][k] = 0.f;
       }
     }
     uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // bits: NaN > inf > finite
-    uint32_t* rd = red[(h - h0) & 1];
-    if (threadIdx.x % 32 == 0) rd[threadIdx.x / 32] = amax;
-    float* sc = scales + static_cast<long long>(pg) * p.heads + h;
+    if (threadIdx.x % 32 == 0) atomicMax(&red[slot], amax);
     const float old = off0 ? *sc : 0.f;             // read by every thread before thread 0 writes it
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) amax = max(amax, rd[w]);
+    amax = red[slot];
+    const int next = slot == 2 ? 0 : slot + 1;
+    if (threadIdx.x == 0) red[next == 2 ? 0 : next + 1] = 0;
+    slot = next;
     float s = page_scale(amax);
     if (off0) s = (old != old || s != s) ? __uint_as_float(0x7fc00000u) : fmaxf(old, s);
     const bool fine = s == s;
-    const float inv = fine ? 1.0f / s : 0.f;        // a power of two: exact
-    uint8_t* pl = pages + (static_cast<long long>(pg) * p.heads + h) * (PAGE * D);
+    // 1 / s, a power of two; 0 for the NaN, whose page gets zeros
+    const float inv = fine ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
     if (off0 && fine && s != old) {                 // the page's older codes follow the scale
       const float g = old * inv;
       for (int q = threadIdx.x; q < off0 * (D / 8); q += THREADS) {
@@ -221,33 +228,32 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
       const int r = row + i * ROWS;
       if (r < cnt) {
         uint8_t* cr = pl + (off0 + r) * D;
-        if (!fine) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) f[i][k] = 0.f;
-        }
         if constexpr (VEC) {
+          const float2 ii = make_float2(inv, inv);
           uint32_t w[4];
           if (half) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float* a = f[i] + 8 * (q & 1) + (q >> 1);
-              w[q] = pack_e4m3x4(make_float2(a[0] * inv, a[2] * inv), make_float2(a[4] * inv, a[6] * inv));
+              w[q] = pack_e4m3x4(__fmul2_rn(make_float2(a[0], a[2]), ii), __fmul2_rn(make_float2(a[4], a[6]), ii));
             }
+            if (!fine) w[0] = w[1] = w[2] = w[3] = 0;
             *reinterpret_cast<uint2*>(cr + 8 * u) = make_uint2(w[0], w[1]);
             *reinterpret_cast<uint2*>(cr + tab.n + 8 * u) = make_uint2(w[2], w[3]);
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const float* a = f[i] + 4 * q;
-              w[q] = pack_e4m3x4(make_float2(a[0] * inv, a[1] * inv), make_float2(a[2] * inv, a[3] * inv));
+              w[q] = pack_e4m3x4(__fmul2_rn(make_float2(a[0], a[1]), ii), __fmul2_rn(make_float2(a[2], a[3]), ii));
             }
+            if (!fine) w[0] = w[1] = w[2] = w[3] = 0;
             *reinterpret_cast<uint4*>(cr + 16 * u) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int2 e = is_v ? make_int2(16 * u + 2 * k, 16 * u + 2 * k + 1) : pair_elems(tab, 8 * u + k);
-            const uint32_t w = pack_e4m3x2(f[i][2 * k] * inv, f[i][2 * k + 1] * inv);
+            const uint32_t w = fine ? pack_e4m3x2(f[i][2 * k] * inv, f[i][2 * k + 1] * inv) : 0u;
             cr[e.x] = static_cast<uint8_t>(w);
             cr[e.y] = static_cast<uint8_t>(w >> 8);
           }
@@ -268,18 +274,19 @@ cudaError_t launch(CacheAppendParams p, const RotaryTable& tab, int num_sms, cud
   p.pages_per_seq = (p.max_new + PAGE - 1) / PAGE + 1;
   const long long gx = static_cast<long long>(p.batch) * p.pages_per_seq;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;
-  // Heads a CTA, which share the sines: one until the grid fills the GPU, then up to 8.
-  long long hpc = gx * 2 * p.heads / (num_sms * 4LL);
-  p.heads_per_cta = static_cast<int>(hpc < 1 ? 1 : (hpc > 8 ? 8 : hpc));
+  // Heads a CTA, which share the sines and hide each other's loads: as many as leave two
+  // CTAs for every SM.
+  const int groups = static_cast<int>(std::min<long long>(p.heads, (2LL * num_sms + 2 * gx - 1) / (2 * gx)));
+  p.heads_per_cta = (p.heads + groups - 1) / groups;
   dim3 grid(static_cast<unsigned>(gx), ceil_div_i(p.heads, p.heads_per_cta), 2);
   using R = Ring<T, D, PAGE>;
   if (!vec) {
-    k_cache_append<T, D, PAGE, false><<<grid, R::THREADS, 0, st>>>(p, tab);
+    k_cache_append<T, D, PAGE, false, false><<<grid, R::THREADS, 0, st>>>(p, tab);
     return cudaGetLastError();
   }
   // As much of the ring as the CTA's heads fill.
   const int smem = R::STAGE * std::min(R::STAGES, p.heads_per_cta);
-  auto kern = k_cache_append<T, D, PAGE, true>;
+  auto kern = tab.half ? k_cache_append<T, D, PAGE, true, true> : k_cache_append<T, D, PAGE, true, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::STAGE * R::STAGES);
   if (e != cudaSuccess) return e;
   kern<<<grid, R::THREADS, smem, st>>>(p, tab);
