@@ -144,11 +144,11 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
         cs[i][k] = r < cnt && 8 * u + k < tab.n ? pairs.cos_sin(8 * u + k, p.pos + (tok0 + r) * tab.naxes, false) : make_float2(1.f, 0.f);
     }
   }
-  // The CTA's maximum of head h: slot h % 3, cleared two heads before.  A slot is read
-  // behind the barrier of its head and cleared behind the next, which everyone reaches
-  // after reading it.
-  __shared__ uint32_t red[3];
-  if (threadIdx.x < 3) red[threadIdx.x] = 0;
+  // The warps' maxima of a head, in turn in one of two rows: a row is written again only
+  // behind the barrier of the head between.
+  static_assert(THREADS <= 1024, "a row of red holds every warp");
+  __shared__ uint32_t red[2][32];
+  if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = 0;
   __syncthreads();
   int slot = 0, stage = 0;
   uint8_t* pl = (is_v ? p.v_pages : p.k_pages) + (static_cast<long long>(pg) * p.heads + h0) * (PAGE * D);
@@ -200,13 +200,11 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
       }
     }
     uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // bits: NaN > inf > finite
-    if (threadIdx.x % 32 == 0) atomicMax(&red[slot], amax);
+    if (threadIdx.x % 32 == 0) red[slot][threadIdx.x / 32] = amax;
     const float old = off0 ? *sc : 0.f;             // read by every thread before thread 0 writes it
     __syncthreads();
-    amax = red[slot];
-    const int next = slot == 2 ? 0 : slot + 1;
-    if (threadIdx.x == 0) red[next == 2 ? 0 : next + 1] = 0;
-    slot = next;
+    amax = __reduce_max_sync(0xffffffffu, red[slot][threadIdx.x % 32]);
+    slot ^= 1;
     float s = page_scale(amax);
     if (off0) s = (old != old || s != s) ? __uint_as_float(0x7fc00000u) : fmaxf(old, s);
     const bool fine = s == s;
