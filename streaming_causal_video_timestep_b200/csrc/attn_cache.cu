@@ -293,24 +293,35 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
 // first of them joins what they found.  A lane holds 4 head dims.
 constexpr int JOIN_WARPS = 8;
 
-template <typename T, int D>
+template <typename T, int D, bool FEW>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
 k_attn_cache_join(const __grid_constant__ AttnCacheParams p, int wpr) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = warp % wpr;
   const long long row = blockIdx.x * static_cast<long long>(JOIN_WARPS / wpr) + warp / wpr;
-  const long long all = static_cast<long long>(p.tokens) * p.heads;
-  const int tok = static_cast<int>(min(row, all - 1) / p.heads), head = static_cast<int>(min(row, all - 1) % p.heads);
-  // Rows of no sequence stay as they are.
-  int lo = 0, hi = p.batch;
-  while (lo < hi) {                               // first b with cu_q[b + 1] > tok
-    const int mid = (lo + hi) / 2;
-    if (p.cu_q[mid + 1] > tok) hi = mid;
-    else lo = mid + 1;
-  }
-  bool on = row < all && lo < p.batch;
-  if (on) {
-    const CacheSeq s = cache_seq(p, lo);
-    on = !s.bad && tok >= s.q0 && tok < s.q0 + s.n;
+  const long long all = FEW ? static_cast<long long>(p.tokens) * p.heads : (p.units - p.full) * 256LL;
+  int tok, head;
+  bool on = row < all;                            // rows of no sequence stay as they are
+  if constexpr (FEW) {
+    tok = static_cast<int>(min(row, all - 1) / p.heads), head = static_cast<int>(min(row, all - 1) % p.heads);
+    int lo = 0, hi = p.batch;
+    while (lo < hi) {                             // first b with cu_q[b + 1] > tok
+      const int mid = (lo + hi) / 2;
+      if (p.cu_q[mid + 1] > tok) hi = mid;
+      else lo = mid + 1;
+    }
+    on = on && lo < p.batch;
+    if (on) {
+      const CacheSeq s = cache_seq(p, lo);
+      on = !s.bad && tok >= s.q0 && tok < s.q0 + s.n;
+    }
+  } else {
+    const CacheUnit u = cache_unit(p, p.full + static_cast<int>(min(row, all - 1) / 256));
+    const CacheSeq s = cache_seq(p, u.b);
+    const int G = p.heads / p.kv_heads;
+    const long long rr = u.pair * 256LL + row % 256;
+    on = on && rr < static_cast<long long>(s.n) * G;
+    tok = s.q0 + static_cast<int>(rr / G);
+    head = u.hk * G + static_cast<int>(rr % G);
   }
   grid_dependency_wait();
   float M = -INFINITY, L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
@@ -368,11 +379,12 @@ cudaError_t launch_rows(const AttnCacheParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <typename T, int D, bool FEW>
 cudaError_t launch_join(const AttnCacheParams& p, cudaStream_t st) {
   int wpr = 1;
   while (wpr < JOIN_WARPS && p.nsplit > 4 * wpr) wpr *= 2;
-  const long long ctas = (static_cast<long long>(p.tokens) * p.heads * wpr + JOIN_WARPS - 1) / JOIN_WARPS;
+  const long long rows = FEW ? static_cast<long long>(p.tokens) * p.heads : (p.units - p.full) * 256LL;
+  const long long ctas = (rows * wpr + JOIN_WARPS - 1) / JOIN_WARPS;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   // Launched while the pieces still run (they say when); waits for their end on the GPU.
   cudaLaunchAttribute at{};
@@ -384,7 +396,7 @@ cudaError_t launch_join(const AttnCacheParams& p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_cache_join<T, D>, p, wpr);
+  return cudaLaunchKernelEx(&cfg, k_attn_cache_join<T, D, FEW>, p, wpr);
 }
 
 }  // namespace
@@ -394,7 +406,13 @@ cudaError_t launch_attn_cache_rows(int dtype, const AttnCacheParams& p, cudaStre
   return p.d == 64 ? launch_rows<__half, 64>(p, st) : launch_rows<__half, 128>(p, st);
 }
 
-cudaError_t launch_attn_cache_join(int dtype, const AttnCacheParams& p, cudaStream_t st) {
-  if (dtype == LA_BF16) return p.d == 64 ? launch_join<__nv_bfloat16, 64>(p, st) : launch_join<__nv_bfloat16, 128>(p, st);
-  return p.d == 64 ? launch_join<__half, 64>(p, st) : launch_join<__half, 128>(p, st);
+template <bool FEW>
+static cudaError_t join_by_type(int dtype, const AttnCacheParams& p, cudaStream_t st) {
+  if (dtype == LA_BF16)
+    return p.d == 64 ? launch_join<__nv_bfloat16, 64, FEW>(p, st) : launch_join<__nv_bfloat16, 128, FEW>(p, st);
+  return p.d == 64 ? launch_join<__half, 64, FEW>(p, st) : launch_join<__half, 128, FEW>(p, st);
+}
+
+cudaError_t launch_attn_cache_join(int dtype, int few, const AttnCacheParams& p, cudaStream_t st) {
+  return few ? join_by_type<true>(dtype, p, st) : join_by_type<false>(dtype, p, st);
 }

@@ -8,10 +8,11 @@
 
 // P is formed as 2^(t - M + P_BIAS), t the score (log2 domain) plus log2 of the
 // value page's scale, M the running maximum of t, raised when t exceeds it by more
-// than P_TAU: P <= 2^15 in fp16, and keeps fp16's 11 bits down to 2^-25 of the
-// largest weighted value (2^-35 in fp16's subnormals).
-#define LA_CACHE_P_BIAS 11.0f
-#define LA_CACHE_P_TAU 4.0f
+// than P_TAU: P <= 2^15 in fp16, and keeps fp16's 11 bits down to 2^-21 of 2^M (2^-31
+// in fp16's subnormals).  A raise rescales O; with 4 for P_TAU it came often enough to
+// cost 2 % at 4680 x 15600 x 40 x 128.
+#define LA_CACHE_P_BIAS 7.0f
+#define LA_CACHE_P_TAU 8.0f
 
 // Programmatic launch: the next grid of the stream may start, and waits here for the
 // end of the grid before it.
@@ -40,6 +41,15 @@ __device__ __forceinline__ int cache_limit(const AttnCacheParams& p, const Cache
   if (p.causal_block == 0) return s.L;
   const long long lim = static_cast<long long>(s.L) - s.n + (r / p.causal_block + 1LL) * p.causal_block;
   return static_cast<int>(max(0LL, min(lim, static_cast<long long>(s.L))));
+}
+// Unit of 256 rows: under a causal mask the last rows of a sequence, which have the most
+// keys, come first.
+struct CacheUnit {
+  int b, hk, pair;
+};
+__device__ __forceinline__ CacheUnit cache_unit(const AttnCacheParams& p, int unit) {
+  const int bh = unit / p.pairs;
+  return {bh / p.kv_heads, bh % p.kv_heads, p.pairs - 1 - unit % p.pairs};
 }
 // Page of the sequence that holds key j (j < L), -1 (and the error word) if the table names none.
 __device__ __forceinline__ int cache_page(const AttnCacheParams& p, int b, int j) {
@@ -85,7 +95,21 @@ template <typename T>
 __device__ __forceinline__ void cache_store4(const AttnCacheParams& p, long long tok, int head, int d4, const float (&a)[4], float L) {
   float v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = L == 0.f ? 0.f : a[e] / L;
+  for (int e = 0; e < 4; ++e) v[e] = a[e] * (L == 0.f ? 0.f : __frcp_rn(L));
   *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + tok * p.o_st + head * p.o_sh + d4) = q_pack4<T>(v);
   if (p.out32) *reinterpret_cast<float4*>(p.out32 + (tok * p.heads + head) * p.d + d4) = make_float4(v[0], v[1], v[2], v[3]);
+}
+// Eight of them.
+template <typename T>
+__device__ __forceinline__ void cache_store8(const AttnCacheParams& p, long long tok, int head, int d8, const float (&a)[8], float L) {
+  if (p.o_vec && !p.out32) {
+    const float inv = L == 0.f ? 0.f : __frcp_rn(L);
+    const float lo[4] = {a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv}, hi[4] = {a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv};
+    const uint2 x = q_pack4<T>(lo), y = q_pack4<T>(hi);
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + tok * p.o_st + head * p.o_sh + d8) = make_uint4(x.x, x.y, y.x, y.y);
+    return;
+  }
+  const float lo[4] = {a[0], a[1], a[2], a[3]}, hi[4] = {a[4], a[5], a[6], a[7]};
+  cache_store4<T>(p, tok, head, d8, lo, L);
+  cache_store4<T>(p, tok, head, d8 + 4, hi, L);
 }

@@ -32,8 +32,8 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int LAUNCH_REGS = 128;            // 65536 / 512
 constexpr int REGS_LOW = 56;                // warps 0-3
-constexpr int REGS_LOAD = 104;              // warps 12-15
-constexpr int REGS_SOFT = 176;              // warps 4-11
+constexpr int REGS_LOAD = 72;               // warps 12-15
+constexpr int REGS_SOFT = 192;              // warps 4-11
 static_assert(128 * (REGS_LOW + REGS_LOAD + 2 * REGS_SOFT) <= THREADS * LAUNCH_REGS, "register split exceeds the launch");
 constexpr uint32_t BOX = 16384;             // 128 rows x 64 fp16, 128-byte swizzle
 constexpr uint32_t TMEM_COLS = 512;
@@ -167,12 +167,15 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
   __shared__ volatile int abort_flag;
 
   if (p.nsplit > 1) launch_dependents();
-  const int b = blockIdx.z, hk = blockIdx.y;
-  const int split = blockIdx.x % p.nsplit;
-  const int pair = gridDim.x / p.nsplit - 1 - blockIdx.x / p.nsplit;   // under a causal mask the last rows have the most keys
+  const int cta = blockIdx.x;
+  const bool whole = cta < p.full;              // else one of the unit's nsplit pieces
+  const int unit = whole ? cta : p.full + (cta - p.full) / p.nsplit;
+  const int split = whole ? 0 : (cta - p.full) % p.nsplit, nsplit = whole ? 1 : p.nsplit;
+  const CacheUnit at_unit = cache_unit(p, unit);
+  const int b = at_unit.b, hk = at_unit.hk, pair = at_unit.pair;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const CacheSeq s = cache_seq(p, b);
-  if (s.bad && blockIdx.x == 0 && hk == 0 && threadIdx.x == 0) raise_device_error(p.err, LA_DEVERR_BAD_DESC);
+  if (s.bad && pair == 0 && split == 0 && hk == 0 && threadIdx.x == 0) raise_device_error(p.err, LA_DEVERR_BAD_DESC);
   const int G = p.heads / p.kv_heads;
   const long long rows = static_cast<long long>(s.n) * G;
   const long long r0 = pair * 256LL;
@@ -181,7 +184,7 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
   const long long last = min(rows, r0 + 256) - 1;
   const int keys = cache_limit(p, s, static_cast<int>(last / G));      // limits do not fall along the rows
   const int tiles = (keys + 127) / 128;
-  const int per = (tiles + p.nsplit - 1) / p.nsplit;
+  const int per = (tiles + nsplit - 1) / nsplit;
   const int t0 = min(split * per, tiles);
   const int nt = min(tiles, t0 + per) - t0;
   int* err = p.err;
@@ -329,7 +332,7 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
     auto unpack = [&](const uint8_t* codes, uint8_t* tile, int t) {
       const float4* sc = sS + (t % NSC) * 4;
       const int left = keys - (t0 + t) * 128;              // rows behind the last key become zeros
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < D / 16; ++i) {
         const int r0 = i * 16 + lw * 4 + (lane >> 3);
         const int r = D == 128 ? r0 ^ hi : 2 * r0 + hi;
@@ -376,39 +379,36 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       const T* q = static_cast<const T*>(p.q) + tok * p.q_st + head * p.q_sh;
       uint8_t* dst = sQ + w * TILE + r * 128;
       uint32_t amax = 0;
-      auto each = [&](auto&& f) {            // f(chunk of 8, its values)
-        if (p.q_vec) {
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (on) u = __ldg(reinterpret_cast<const uint4*>(q) + c);
-            const T* e = reinterpret_cast<const T*>(&u);
-            float v[8];
+      uint4 raw_q[D / 8];                    // the row, all of it under way at once
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = q_to_f32(e[k]);
-            f(c, v);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < D / 8; ++c) {
-            float v[8];
+      for (int c = 0; c < D / 8; ++c) {
+        raw_q[c] = make_uint4(0, 0, 0, 0);
+        if (on && p.q_vec) raw_q[c] = __ldg(reinterpret_cast<const uint4*>(q) + c);
+      }
+      if (on && !p.q_vec) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = on ? q_to_f32(q[8 * c + k]) : 0.f;
-            f(c, v);
-          }
+        for (int c = 0; c < D / 8; ++c) {
+          T e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) e[k] = q[8 * c + k];
+          raw_q[c] = *reinterpret_cast<uint4*>(e);
         }
-      };
-      each([&](int, const float (&v)[8]) {
+      }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max(amax, __float_as_uint(v[k]) & 0x7fffffffu);
-      });
+      for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          amax = max(amax, __float_as_uint(q_to_f32(reinterpret_cast<const T*>(&raw_q[c])[k])) & 0x7fffffffu);
       const float g = q_row_scale(amax);
       rowf = p.scale_log2 / g;
-      each([&](int c, const float (&v)[8]) {
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = q_to_f32(reinterpret_cast<const T*>(&raw_q[c])[k]) * g;
         *reinterpret_cast<uint4*>(dst + (c >> 3) * BOX + (((c & 7) ^ (r & 7)) << 4)) =
-            make_uint4(pack_f16x2(v[0] * g, v[1] * g), pack_f16x2(v[2] * g, v[3] * g), pack_f16x2(v[4] * g, v[5] * g),
-                       pack_f16x2(v[6] * g, v[7] * g));
-      });
+            make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -451,10 +451,10 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
         if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (!ok) abort_flag = 1;
-      const long long part = (static_cast<long long>(split) * p.tokens + tok) * p.heads + head;
+      const long long part = (static_cast<long long>(split) * (p.units - p.full) + unit - p.full) * 256 + w * 128 + r;
       if (ok && (nt == 0 || mbar_wait(&pv_done[w], 0, err))) {
         tc_fence_after();
-        if (p.nsplit > 1 && on) p.part_ml[part] = make_float2(m_ref, l);
+        if (!whole && on) p.part_ml[part] = make_float2(m_ref, l);
 #pragma unroll 1
         for (int c4 = 0; c4 < D / 32; ++c4) {
           uint32_t o[32];
@@ -467,13 +467,17 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
           }
           if (on) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float v[4] = {__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                  __uint_as_float(o[4 * i + 3])};
-              if (p.nsplit > 1)
-                *reinterpret_cast<float4*>(p.part_o + part * D + c4 * 32 + 4 * i) = make_float4(v[0], v[1], v[2], v[3]);
-              else
-                cache_store4<T>(p, tok, head, c4 * 32 + 4 * i, v, l);
+            for (int i = 0; i < 4; ++i) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[8 * i + k]);
+              if (!whole) {
+                float4* to = reinterpret_cast<float4*>(p.part_o + part * D + c4 * 32 + 8 * i);
+                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+              } else {
+                cache_store8<T>(p, tok, head, c4 * 32 + 8 * i, v, l);
+              }
             }
           }
         }
@@ -505,10 +509,9 @@ cudaError_t launch(const AttnCacheParams& p, cudaStream_t st) {
   }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(p.max_q) * (p.heads / p.kv_heads);
-  const long long gx = (rows + 255) / 256 * p.nsplit;
+  const long long gx = p.full + static_cast<long long>(p.units - p.full) * p.nsplit;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kern<<<dim3(static_cast<unsigned>(gx), p.kv_heads, p.batch), THREADS, SMEM, st>>>(p);
+  kern<<<static_cast<unsigned>(gx), THREADS, SMEM, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -178,13 +178,16 @@ struct AttnCacheParams {
   int tokens, batch, heads, kv_heads, d, page_tokens, num_pages, max_pages, max_q, causal_block;
   float scale_log2;                    // softmax scale * log2(e)
   int page_shift;                      // log2(page_tokens)
-  int q_vec;                           // q's rows are 16-byte aligned
-  int nsplit;                          // pieces of the key axis
-  float* part_o; float2* part_ml;      // nsplit > 1: [nsplit, tokens, heads, d], [nsplit, tokens, heads]
+  int q_vec, o_vec;                    // q's, out's rows are 16-byte aligned
+  // Few rows: every row's keys in nsplit pieces, part_* [nsplit, tokens * heads] rows.
+  // Many rows: units of 256 rows of a (sequence, key head), pairs of them each; the first
+  // `full` whole, the others in nsplit pieces, part_* [nsplit, (units - full) * 256] rows.
+  int nsplit, pairs, full, units;
+  float* part_o; float2* part_ml;      // nsplit > 1: a row's d sums, and (maximum, normaliser)
   int* err;
 };
 // Few rows (max_q * heads / kv_heads <= LA_CACHE_FEW_ROWS) and the join of split keys; many rows.
 #define LA_CACHE_FEW_ROWS 16
 cudaError_t launch_attn_cache_rows(int dtype, const AttnCacheParams& p, cudaStream_t st);
-cudaError_t launch_attn_cache_join(int dtype, const AttnCacheParams& p, cudaStream_t st);
+cudaError_t launch_attn_cache_join(int dtype, int few, const AttnCacheParams& p, cudaStream_t st);
 cudaError_t launch_attn_cache_tc(int dtype, const AttnCacheParams& p, cudaStream_t st);

@@ -65,27 +65,41 @@ bool cache_fine(const la_paged_cache* c) {
 
 bool few_rows(int64_t max_q, int32_t heads, int32_t kv_heads) { return max_q * (heads / kv_heads) <= LA_CACHE_FEW_ROWS; }
 
-// Pieces of the key axis.  Few rows: enough CTAs for 3 on every SM with at least 128
-// keys each (16 streams of one token over 1561 keys: 9.7 us; 10.9 with 256), and
-// pieces of about 2048 keys where that makes more, which evens out ragged lengths
-// (16 x 40 heads over up to 14040 keys: 258 us; 343 unsplit, 285 with 1024 keys).
-// Many rows (one CTA an SM, 256 rows each): the number of pieces that makes the
-// fewest key tiles in a row on the busiest SM, a piece counted two tiles longer than
-// it is for its start and end and its part of the join.
-int plan_split(int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
-  const int64_t rows = max_q * (heads / kv_heads);
+// How a call is laid out.  Few rows: enough CTAs for 3 on every SM with at least 128
+// keys each (one token over 1561 keys x 8 heads: 9.7 us; 10.9 with 256), and pieces of
+// about 2048 keys where that makes more, which evens out ragged lengths (16 x 40 heads
+// over up to 14040 keys: 258 us; 343 unsplit, 285 with 1024 keys).
+// Many rows: one CTA an SM, 256 rows of a (sequence, key head) each.  The units behind
+// the last full round of the SMs are split along the keys, into the number of pieces that
+// makes the fewest key tiles in a row, a piece counted two tiles longer than it is for
+// its start and end and its part of the join (760 units of 122 tiles: MANY_BEFORE us
+// unsplit, MANY_AFTER with the last 20 in 7 pieces each).
+struct Plan {
+  int nsplit = 1, pairs = 0, full = 0, units = 0;
+  int64_t part_rows = 0;                           // of all pieces
+};
+constexpr int kSms = 148;
+
+bool plan_call(Plan& pl, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
   if (few_rows(max_q, heads, kv_heads)) {
-    const int64_t ctas = static_cast<int64_t>(kv_heads) * batch, want = 148 * 3;
-    return static_cast<int>(std::max({int64_t{1}, std::min((want + ctas - 1) / ctas, max_kv / 128), max_kv / 2048}));
+    const int64_t ctas = static_cast<int64_t>(kv_heads) * batch;
+    pl.nsplit = static_cast<int>(std::max({int64_t{1}, std::min((kSms * 3 + ctas - 1) / ctas, max_kv / 128), max_kv / 2048}));
+    pl.part_rows = pl.nsplit > 1 ? pl.nsplit * tokens * heads : 0;
+    return true;
   }
-  const int64_t ctas = (rows + 255) / 256 * kv_heads * batch, tiles = (max_kv + 127) / 128;
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int n = 1; n <= 1; ++n) {
-    const int64_t cost = (ctas * n + 147) / 148 * ((tiles + n - 1) / n + 2);
-    if (cost < best_cost) best_cost = cost, best = n;
+  const int64_t pairs = (max_q * (heads / kv_heads) + 255) / 256, units = pairs * kv_heads * batch;
+  if (units > (1 << 28)) return false;
+  const int64_t tail = units % kSms, tiles = (max_kv + 127) / 128;
+  int64_t best = INT64_MAX;
+  for (int n = 1; n <= 32 && tail > 0 && (n == 1 || tiles / n >= 4); ++n) {
+    const int64_t cost = (tail * n + kSms - 1) / kSms * ((tiles + n - 1) / n + 2);
+    if (cost < best) best = cost, pl.nsplit = n;
   }
-  return best;
+  pl.pairs = static_cast<int>(pairs);
+  pl.units = static_cast<int>(units);
+  pl.full = static_cast<int>(pl.nsplit > 1 ? units - tail : units);
+  pl.part_rows = pl.nsplit > 1 ? pl.nsplit * tail * 256 : 0;
+  return true;
 }
 
 }  // namespace
@@ -166,8 +180,9 @@ int64_t la_op_attention_cache_fp8_workspace(const la_paged_cache* cache, int64_t
   if (!cache_fine(cache) || heads < 1 || heads % cache->heads != 0 || tokens < 0 || tokens > kMaxRows || max_q < 0 ||
       max_q > kMaxRows || max_kv < 0 || max_kv > kMaxRows)
     return LA_EINVAL;
-  const int n = plan_split(std::min(max_q, tokens), max_kv, cache->batch, heads, cache->heads);
-  return n == 1 ? 0 : n * tokens * heads * (cache->head_dim * 4LL + 8);
+  Plan pl;
+  if (!plan_call(pl, tokens, std::min(max_q, tokens), max_kv, cache->batch, heads, cache->heads)) return LA_EINVAL;
+  return pl.part_rows * (cache->head_dim * 4LL + 8);
 }
 
 int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const void* q, int64_t q_token_stride,
@@ -194,6 +209,7 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
   p.out = out;
   p.out32 = out32;
   p.q_vec = aligned(q, 16) && q_token_stride % 8 == 0 && q_head_stride % 8 == 0;
+  p.o_vec = aligned(out, 16) && out_token_stride % 8 == 0 && out_head_stride % 8 == 0;
   p.q_st = q_token_stride;
   p.q_sh = q_head_stride;
   p.o_st = out_token_stride;
@@ -217,16 +233,21 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
   p.max_q = static_cast<int>(std::min(max_q, tokens));
   p.causal_block = causal_block;
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-  p.nsplit = plan_split(p.max_q, max_kv, p.batch, heads, cache->heads);
+  Plan pl;
+  if (!plan_call(pl, tokens, p.max_q, max_kv, p.batch, heads, cache->heads)) return LA_EINVAL;
+  p.nsplit = pl.nsplit;
+  p.pairs = pl.pairs;
+  p.full = pl.full;
+  p.units = pl.units;
   if (p.nsplit > 1) {
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + p.nsplit * tokens * heads * p.d);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + pl.part_rows * p.d);
   }
   if (op_error_word(&p.err) != LA_OK) return LA_ECUDA;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = few_rows(p.max_q, heads, cache->heads) ? launch_attn_cache_rows(dtype, p, st)
-                                                         : launch_attn_cache_tc(dtype, p, st);
-  if (e == cudaSuccess && p.nsplit > 1) e = launch_attn_cache_join(dtype, p, st);
+  const bool few = few_rows(p.max_q, heads, cache->heads);
+  cudaError_t e = few ? launch_attn_cache_rows(dtype, p, st) : launch_attn_cache_tc(dtype, p, st);
+  if (e == cudaSuccess && p.nsplit > 1) e = launch_attn_cache_join(dtype, few, p, st);
   return ret(e);
 }
 
