@@ -31,9 +31,9 @@ namespace {
 
 constexpr int THREADS = 512;
 constexpr int LAUNCH_REGS = 128;            // 65536 / 512
-constexpr int REGS_LOW = 56;                // warps 0-3
-constexpr int REGS_LOAD = 72;               // warps 12-15
-constexpr int REGS_SOFT = 192;              // warps 4-11
+constexpr int REGS_LOW = 96;                // warps 0-3
+constexpr int REGS_LOAD = 96;               // warps 12-15
+constexpr int REGS_SOFT = 160;              // warps 4-11
 static_assert(128 * (REGS_LOW + REGS_LOAD + 2 * REGS_SOFT) <= THREADS * LAUNCH_REGS, "register split exceeds the launch");
 constexpr uint32_t BOX = 16384;             // 128 rows x 64 fp16, 128-byte swizzle
 constexpr uint32_t TMEM_COLS = 512;
@@ -42,6 +42,8 @@ static_assert(NSC >= 4 + 2, "the scales outlast the K ring and the tile of codes
 
 template <int D> __host__ __device__ constexpr uint32_t tile_bytes() { return D / 64 * BOX; }
 template <int D> __host__ __device__ constexpr int stages() { return D == 64 ? 4 : 2; }
+// Parts in which a tile's P is handed to the tensor core.
+template <int D> __host__ __device__ constexpr int hands() { return D == 64 ? 2 : 1; }
 template <int D> __host__ __device__ constexpr size_t smem_bytes() {
   return 1024 + 2 * tile_bytes<D>() + stages<D>() * 2 * tile_bytes<D>() + 2 * 128 * D + NSC * 64 + 512;
 }
@@ -75,21 +77,20 @@ __device__ __forceinline__ void ld_wait(uint32_t (&u)[32]) {
                  "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31])::"memory");
 }
 
-// One row's scores of a key tile (raw accumulators in tensor memory) to P (fp16
-// pairs), written over them, and the row's share of the normaliser.  The scores are
-// read twice, 32 at a time, once for the maximum: 128 of them held at once would not
-// fit beside the loaders' registers (chunk c of P lies in chunk c / 2 of the scores,
-// which the second pass has read by then).  sc[c]: the chunk's (ks, log2 vs, 1 / vs).
+// The running maximum of a row over a key tile's scores (raw accumulators in tensor
+// memory, log2 domain with the value scale) and what it makes of the old one.  sc[c]: a
+// 32-key chunk's (ks, log2 vs, 1 / vs).  The scores are read twice, 32 at a time, once
+// here: 128 of them held at once would not fit beside the other warps' registers.
 template <bool MASKED>
-__device__ __forceinline__ float softmax_tile(uint32_t s_base, int valid, float rowf, const float4* sc, float& m_ref,
-                                              float& alpha) {
+__device__ __forceinline__ void softmax_max(uint32_t s_base, int valid, float rowf, const float4* sc, float& m_ref,
+                                            float& alpha) {
   uint32_t u[2][32];
-  float a[4], mt = -INFINITY;
+  float mt = -INFINITY;
   tmem_ld32(s_base, u[0]);
   ld_wait(u[0]);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    tmem_ld32(s_base + (c + 1) % 4 * 32, u[(c + 1) & 1]);
+    if (c < 3) tmem_ld32(s_base + (c + 1) * 32, u[(c + 1) & 1]);
     float m[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -102,37 +103,48 @@ __device__ __forceinline__ float softmax_tile(uint32_t s_base, int valid, float 
       m[k] = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
     }
     const float2 v = *reinterpret_cast<const float2*>(sc + c);
-    a[c] = v.x * rowf;
-    mt = fmaxf(mt, fmaf(max3(fmaxf(m[0], m[1]), m[2], m[3]), a[c], v.y));
-    ld_wait(u[(c + 1) & 1]);
+    mt = fmaxf(mt, fmaf(max3(fmaxf(m[0], m[1]), m[2], m[3]), v.x * rowf, v.y));
+    if (c < 3) ld_wait(u[(c + 1) & 1]);
   }
   const bool need = mt > m_ref + LA_CACHE_P_TAU;
   const float mn = need ? mt : m_ref;
   alpha = need ? fast_exp2(m_ref - mn) : 1.0f;
   m_ref = mn;
-  const float base = LA_CACHE_P_BIAS - (mn == -INFINITY ? 0.f : mn);
+}
+
+// The row's P (fp16 pairs) of 64 keys, chunks c0 and c0 + 1, stored over scores that both
+// passes have read by then (P of chunk c lies in chunk c / 2 of the scores), and their
+// share of the normaliser.
+template <bool MASKED>
+__device__ __forceinline__ float softmax_exp(uint32_t s_base, int c0, int valid, float rowf, const float4* sc, float m_ref) {
+  uint32_t u[2][32];
+  const float base = LA_CACHE_P_BIAS - (m_ref == -INFINITY ? 0.f : m_ref);
   float l = 0.f;
+  tmem_ld32(s_base + c0 * 32, u[0]);
+  tmem_ld32(s_base + c0 * 32 + 32, u[1]);
+  ld_wait(u[0]);
+  ld_wait(u[1]);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (c < 3) tmem_ld32(s_base + (c + 1) * 32, u[(c + 1) & 1]);
-    const float2 v = make_float2(sc[c].y, sc[c].z);
-    const float2 aa = make_float2(a[c], a[c]), off = make_float2(base + v.x, base + v.x);
+  for (int k = 0; k < 2; ++k) {
+    const int c = c0 + k;
+    const float4 v = sc[c];
+    const float a = v.x * rowf;
+    const float2 aa = make_float2(a, a), off = make_float2(base + v.y, base + v.y);
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     uint32_t P[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 x = __ffma2_rn(make_float2(__uint_as_float(u[c & 1][2 * i]), __uint_as_float(u[c & 1][2 * i + 1])), aa, off);
-      float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(u[k][2 * i]), __uint_as_float(u[k][2 * i + 1])), aa, off);
+      float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
       if (MASKED) {                            // a masked key is 0, whatever its page's scale
-        if (32 * c + 2 * i >= valid) p.x = 0.f;
-        if (32 * c + 2 * i + 1 >= valid) p.y = 0.f;
+        if (32 * c + 2 * i >= valid) e.x = 0.f;
+        if (32 * c + 2 * i + 1 >= valid) e.y = 0.f;
       }
-      acc[i & 1] = __fadd2_rn(acc[i & 1], p);
-      P[i] = pack_f16x2(p.x, p.y);
+      acc[i & 1] = __fadd2_rn(acc[i & 1], e);
+      P[i] = pack_f16x2(e.x, e.y);
     }
     const float2 t = __fadd2_rn(acc[0], acc[1]);
-    if (!MASKED || 32 * c < valid) l = fmaf(t.x + t.y, v.y, l);
-    if (c < 3) ld_wait(u[(c + 1) & 1]);
+    if (!MASKED || 32 * c < valid) l = fmaf(t.x + t.y, v.z, l);
     tmem_st16(s_base + 16 * c, P);
   }
   return l;
@@ -160,8 +172,8 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
   uint64_t* raw_full = sc_full + NSC;       // K, V
   uint64_t* raw_empty = raw_full + 2;       // K, V
   uint64_t* s_full = raw_empty + 2;         // [2]
-  uint64_t* p_full = s_full + 2;            // [2]
-  uint64_t* pv_done = p_full + 2;           // [2]
+  uint64_t* p_full = s_full + 2;            // [tile][half of its keys]
+  uint64_t* pv_done = p_full + 4;           // [2]
   uint64_t* drain = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ volatile int abort_flag;
@@ -203,7 +215,8 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       mbar_init(&raw_full[w], 1);
       mbar_init(&raw_empty[w], 4);
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 4);
+      mbar_init(&p_full[2 * w], 4);
+      mbar_init(&p_full[2 * w + 1], 4);
       mbar_init(&pv_done[w], 1);
     }
     mbar_init(drain, 1);
@@ -298,17 +311,23 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
         const uint32_t vs = t % NS, vpar = (t / NS) & 1, ks = (t + 1) % NS, kpar = ((t + 1) / NS) & 1;
         ok = wwait(&v_full[vs], vpar) && (!more || wwait(&k_full[ks], kpar));
         for (int w = 0; w < nq && ok; ++w) {
-          if (!wwait(&p_full[w], static_cast<uint32_t>(t & 1))) { ok = false; break; }
-          tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_ts(tmem + o_col(w), tmem + s_col(w) + kk * 8, dV + ((vs * TILE + kk * 2048) >> 4), idPV,
-                           (t > 0 || kk > 0) ? 1u : 0u);
-            if (more) issue_s(w, ks);
-            else umma_commit(&pv_done[w]);
+          for (int h = 0; h < hands<D>(); ++h) {
+            ok = ok && wwait(&p_full[2 * w + h], static_cast<uint32_t>(t & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = h * (8 / hands<D>()); kk < (h + 1) * (8 / hands<D>()); ++kk)
+                umma_bf16_ts(tmem + o_col(w), tmem + s_col(w) + kk * 8, dV + ((vs * TILE + kk * 2048) >> 4), idPV,
+                             (t > 0 || kk > 0) ? 1u : 0u);
+              if (h == hands<D>() - 1) {
+                if (more) issue_s(w, ks);
+                else umma_commit(&pv_done[w]);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (!ok) break;
         if (elect_one()) {
@@ -429,26 +448,35 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
         tc_fence_after();
         float alpha;
         const float4* sc = sS + (t % NSC) * 4;
-        const float rs = __all_sync(0xffffffffu, valid >= 128)
-                             ? softmax_tile<false>(s_base, valid, rowf, sc, m_ref, alpha)
-                             : softmax_tile<true>(s_base, valid, rowf, sc, m_ref, alpha);
+        const bool full = __all_sync(0xffffffffu, valid >= 128);
+        if (full) softmax_max<false>(s_base, valid, rowf, sc, m_ref, alpha);
+        else softmax_max<true>(s_base, valid, rowf, sc, m_ref, alpha);
         if (t >= 1 && __any_sync(0xffffffffu, alpha != 1.0f)) {
           // O is stable: the commit that signalled S(t) also covers PV(t-1), issued before it
 #pragma unroll 1
           for (int c4 = 0; c4 < D / 32; ++c4) {
             uint32_t o[32];
             tmem_ld32(o_base + c4 * 32, o);
-            tmem_ld_wait();
+            ld_wait(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
             tmem_st32(o_base + c4 * 32, o);
           }
         }
-        tmem_st_wait();
-        l = l * alpha + rs;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
+        // At D = 64 the first half of P is handed over as soon as it is there: its products
+        // run beside the second half's exponentials (4 prompts of up to 1013 rows: 108 us,
+        // 114 in one).  At D = 128 that was slower (1717 us at 4680 x 15600 x 40, 1567).
+        l *= alpha;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          l += full ? softmax_exp<false>(s_base, 2 * h, valid, rowf, sc, m_ref)
+                    : softmax_exp<true>(s_base, 2 * h, valid, rowf, sc, m_ref);
+          if (hands<D>() == 1 && h == 0) continue;
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * w + (hands<D>() == 1 ? 0 : h)]);
+        }
       }
       if (!ok) abort_flag = 1;
       const long long part = (static_cast<long long>(split) * (p.units - p.full) + unit - p.full) * 256 + w * 128 + r;
