@@ -83,7 +83,7 @@ constexpr int kSms = 148;
 bool plan_call(Plan& pl, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
   if (few_rows(max_q, heads, kv_heads)) {
     const int64_t ctas = static_cast<int64_t>(kv_heads) * batch;
-    pl.nsplit = static_cast<int>(std::max({int64_t{1}, std::min((kSms * 3 + ctas - 1) / ctas, max_kv / 128), max_kv / 2048}));
+    pl.nsplit = static_cast<int>(std::max({int64_t{1}, std::min((kSms * 3 + ctas - 1) / ctas, max_kv / 128), std::min<int64_t>(max_kv / 2048, 1024)}));
     pl.part_rows = pl.nsplit > 1 ? pl.nsplit * tokens * heads : 0;
     return true;
   }
