@@ -30,6 +30,8 @@ What it computes (Live Avatar, arXiv 2512.04677, as described on the pages):
     and per-row e4m3 quantization with the FP8 GEMM plus FP8 attention
     (oracle/fp8.py) for the operator-optimisation row (papernotes note, the
     paper's Table 3);
+  * rotary positions with several axes, the paged e4m3 cache's append and
+    attention over it (oracle/cache8.py; no counterpart on the pages);
   * the full synthetic DiT block (oracle/dit.py): AdaLN-modulated attention
     and tanh-GELU FFN sub-blocks with gated residuals (a reading after the
     Wan-style block the model is built on; the pages give no internals).

@@ -279,7 +279,7 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     }
     const int tok = s.q0 + (r0 + r) / G, head = hk * G + (r0 + r) % G;
     if (p.nsplit > 1) {
-      const long long row = (static_cast<long long>(split) * p.tokens + tok) * p.heads + head;
+      const long long row = (static_cast<long long>(split) * p.batch + b) * p.max_q * p.heads + (r0 + r) / G * p.heads + head;
       *reinterpret_cast<float4*>(p.part_o + row * D + d4) = make_float4(a[0], a[1], a[2], a[3]);
       if (d4 == 0) p.part_ml[row] = make_float2(M, L);
     } else {
@@ -300,31 +300,25 @@ __global__ void __launch_bounds__(JOIN_MAX_WARPS * 32)
 k_attn_cache_join(const __grid_constant__ AttnCacheParams p, int wpr) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = warp % wpr;
   const long long row = blockIdx.x * static_cast<long long>(blockDim.x / 32 / wpr) + warp / wpr;
-  const long long all = FEW ? static_cast<long long>(p.tokens) * p.heads : (p.units - p.full) * 256LL;
-  int tok, head;
-  bool on = row < all;                            // rows of no sequence stay as they are
+  const long long all = FEW ? static_cast<long long>(p.batch) * p.max_q * p.heads : (p.units - p.full) * 256LL;
+  const long long at = min(row, all - 1);
+  const int G = p.heads / p.kv_heads;
+  int b, head;
+  long long q;                                    // query of the sequence
   if constexpr (FEW) {
-    tok = static_cast<int>(min(row, all - 1) / p.heads), head = static_cast<int>(min(row, all - 1) % p.heads);
-    int lo = 0, hi = p.batch;
-    while (lo < hi) {                             // first b with cu_q[b + 1] > tok
-      const int mid = (lo + hi) / 2;
-      if (p.cu_q[mid + 1] > tok) hi = mid;
-      else lo = mid + 1;
-    }
-    on = on && lo < p.batch;
-    if (on) {
-      const CacheSeq s = cache_seq(p, lo);
-      on = !s.bad && tok >= s.q0 && tok < s.q0 + s.n;
-    }
+    b = static_cast<int>(at / (p.max_q * p.heads));
+    head = static_cast<int>(at % p.heads);
+    q = at / p.heads % p.max_q;
   } else {
-    const CacheUnit u = cache_unit(p, p.full + static_cast<int>(min(row, all - 1) / 256));
-    const CacheSeq s = cache_seq(p, u.b);
-    const int G = p.heads / p.kv_heads;
-    const long long rr = u.pair * 256LL + row % 256;
-    on = on && rr < static_cast<long long>(s.n) * G;
-    tok = s.q0 + static_cast<int>(rr / G);
+    const CacheUnit u = cache_unit(p, p.full + static_cast<int>(at / 256));
+    const long long rr = u.pair * 256LL + at % 256;
+    b = u.b;
     head = u.hk * G + static_cast<int>(rr % G);
+    q = rr / G;
   }
+  const CacheSeq s = cache_seq(p, b);
+  const bool on = row < all && q < s.n;           // rows of no sequence stay as they are
+  const long long tok = s.q0 + q;
   grid_dependency_wait();
   float M = -INFINITY, L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
   const int d4 = lane * 4;
@@ -395,7 +389,7 @@ cudaError_t launch_join(const AttnCacheParams& p, cudaStream_t st) {
   int wpr = 1;
   while (wpr < JOIN_MAX_WARPS && p.nsplit > 4 * wpr) wpr *= 2;
   const int warps = wpr > JOIN_WARPS ? wpr : JOIN_WARPS;
-  const long long rows = FEW ? static_cast<long long>(p.tokens) * p.heads : (p.units - p.full) * 256LL;
+  const long long rows = FEW ? static_cast<long long>(p.batch) * p.max_q * p.heads : (p.units - p.full) * 256LL;
   const long long ctas = (rows * wpr + warps - 1) / warps;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   // Launched while the pieces still run (they say when); waits for their end on the GPU.

@@ -9,6 +9,11 @@
 // each thread reads back what it copied, so nothing waits for another thread but the
 // reduction).  Bound: HBM.
 //
+// An element on the border between two codes goes to one or the other by the last bit of
+// its rotation, so that is the fp32 definition's to the bit: sine and cosine nearest to
+// the exact ones (in fp64, once for all the heads of a CTA), each product and sum
+// rounded by itself.
+//
 // Scale: 2^k, the smallest with 448 * 2^k >= amax (k >= -64), read off amax's own
 // exponent and mantissa, so no rounding decides it.  A page that already holds
 // tokens keeps the larger of its scale and that; where it grows, the codes in
@@ -141,7 +146,7 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
       const int r = row + i * ROWS;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        cs[i][k] = r < cnt && 8 * u + k < tab.n ? pairs.cos_sin(8 * u + k, p.pos + (tok0 + r) * tab.naxes, false) : make_float2(1.f, 0.f);
+        cs[i][k] = r < cnt && 8 * u + k < tab.n ? pairs.cos_sin_nearest(8 * u + k, p.pos + (tok0 + r) * tab.naxes) : make_float2(1.f, 0.f);
     }
   }
   // The warps' maxima of a head, in turn in one of two rows: a row is written again only
@@ -191,8 +196,8 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float v = f[i][2 * k], w = f[i][2 * k + 1];
-            f[i][2 * k] = v * cs[i][k].x - w * cs[i][k].y;
-            f[i][2 * k + 1] = v * cs[i][k].y + w * cs[i][k].x;
+            f[i][2 * k] = __fsub_rn(__fmul_rn(v, cs[i][k].x), __fmul_rn(w, cs[i][k].y));
+            f[i][2 * k + 1] = __fadd_rn(__fmul_rn(v, cs[i][k].y), __fmul_rn(w, cs[i][k].x));
           }
         }
 #pragma unroll

@@ -179,7 +179,7 @@ struct AttnCacheParams {
   float scale_log2;                    // softmax scale * log2(e)
   int page_shift;                      // log2(page_tokens)
   int q_vec, o_vec;                    // q's, out's rows are 16-byte aligned
-  // Few rows: every row's keys in nsplit pieces, part_* [nsplit, tokens * heads] rows.
+  // Few rows: every row's keys in nsplit pieces, part_* [nsplit, batch, max_q, heads] rows.
   // Many rows: units of 256 rows of a (sequence, key head), pairs of them each; the first
   // `full` whole, the others in nsplit pieces, part_* [nsplit, (units - full) * 256] rows.
   int nsplit, pairs, full, units;

@@ -54,6 +54,11 @@ bool strides_fit(int64_t rows, int64_t st, int64_t sh, int32_t heads, int32_t d)
   return st >= 0 && sh >= 0 && (heads == 1 || sh >= d) && (rows <= 1 || st >= 1) && st <= (1LL << 40) && sh <= (1LL << 40);
 }
 
+// An output's rows do not lie over one another: one of the two strides steps over all of the other's.
+bool rows_apart(int64_t rows, int64_t st, int64_t sh, int32_t heads, int32_t d) {
+  return rows <= 1 || st >= (heads - 1) * sh + d || (heads == 1 ? st >= d : st >= d && sh >= (rows - 1) * st + d);
+}
+
 bool cache_fine(const la_paged_cache* c) {
   if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->block_table) return false;
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return false;
@@ -80,11 +85,11 @@ struct Plan {
 };
 constexpr int kSms = 148;
 
-bool plan_call(Plan& pl, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
+bool plan_call(Plan& pl, int64_t max_q, int64_t max_kv, int32_t batch, int32_t heads, int32_t kv_heads) {
   if (few_rows(max_q, heads, kv_heads)) {
     const int64_t ctas = static_cast<int64_t>(kv_heads) * batch;
     pl.nsplit = static_cast<int>(std::max({int64_t{1}, std::min((kSms * 3 + ctas - 1) / ctas, max_kv / 128), std::min<int64_t>(max_kv / 2048, 1024)}));
-    pl.part_rows = pl.nsplit > 1 ? pl.nsplit * tokens * heads : 0;
+    pl.part_rows = pl.nsplit > 1 ? pl.nsplit * batch * max_q * heads : 0;
     return true;
   }
   const int64_t pairs = (max_q * (heads / kv_heads) + 255) / 256, units = pairs * kv_heads * batch;
@@ -113,7 +118,8 @@ int la_op_rope_axes(int32_t dtype, const void* x, int64_t x_token_stride, int64_
   if (!known_dtype(dtype) || tokens < 0 || tokens > kMaxRows || heads < 1 || heads > 65535) return LA_EINVAL;
   if (head_dim < 2 || head_dim > 2 * LA_ROPE_MAX_PAIRS || naxes < 1) return LA_EINVAL;
   if (!strides_fit(tokens, x_token_stride, x_head_stride, heads, head_dim) ||
-      !strides_fit(tokens, out_token_stride, out_head_stride, heads, head_dim))
+      !strides_fit(tokens, out_token_stride, out_head_stride, heads, head_dim) ||
+      !rows_apart(tokens, out_token_stride, out_head_stride, heads, head_dim))
     return LA_EINVAL;
   RotaryTable tab;
   if (!fill_table(tab, head_dim, naxes, pairs, theta, half, inverse)) return LA_EINVAL;
@@ -181,7 +187,7 @@ int64_t la_op_attention_cache_fp8_workspace(const la_paged_cache* cache, int64_t
       max_q > kMaxRows || max_kv < 0 || max_kv > kMaxRows)
     return LA_EINVAL;
   Plan pl;
-  if (!plan_call(pl, tokens, std::min(max_q, tokens), max_kv, cache->batch, heads, cache->heads)) return LA_EINVAL;
+  if (!plan_call(pl, std::min(max_q, tokens), max_kv, cache->batch, heads, cache->heads)) return LA_EINVAL;
   return pl.part_rows * (cache->head_dim * 4LL + 8);
 }
 
@@ -195,7 +201,8 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
       max_kv < 0 || max_kv > kMaxRows || causal_block < 0 || !(scale > 0.0 && scale < 1e30))
     return LA_EINVAL;
   if (!strides_fit(tokens, q_token_stride, q_head_stride, heads, cache->head_dim) ||
-      !strides_fit(tokens, out_token_stride, out_head_stride, heads, cache->head_dim))
+      !strides_fit(tokens, out_token_stride, out_head_stride, heads, cache->head_dim) ||
+      !rows_apart(tokens, out_token_stride, out_head_stride, heads, cache->head_dim))
     return LA_EINVAL;
   if (!cu_q || !kv_len) return LA_EINVAL;
   const int64_t need = la_op_attention_cache_fp8_workspace(cache, tokens, heads, max_q, max_kv);
@@ -234,7 +241,7 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
   p.causal_block = causal_block;
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
   Plan pl;
-  if (!plan_call(pl, tokens, p.max_q, max_kv, p.batch, heads, cache->heads)) return LA_EINVAL;
+  if (!plan_call(pl, p.max_q, max_kv, p.batch, heads, cache->heads)) return LA_EINVAL;
   p.nsplit = pl.nsplit;
   p.pairs = pl.pairs;
   p.full = pl.full;

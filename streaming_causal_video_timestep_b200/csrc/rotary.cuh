@@ -55,6 +55,13 @@ struct PairTable {
     const float2 v = turn_cos_sin(static_cast<uint32_t>(ph >> 32));
     return make_float2(v.x, inverse ? -v.y : v.y);
   }
+  // The same, each the fp32 value nearest to the exact one (computed in fp64).
+  __device__ __forceinline__ float2 cos_sin_nearest(int j, const int* pos) const {
+    const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos[axis[j]])) * turn[j];
+    double s, c;
+    sincospi(static_cast<double>(static_cast<long long>(ph)) * 1.0842021724855044e-19 /* 2^-63 */, &s, &c);
+    return make_float2(static_cast<float>(c), static_cast<float>(s));
+  }
 };
 
 template <typename T> struct Vec16;             // 16 bytes of T as fp32 values

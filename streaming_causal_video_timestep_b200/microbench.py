@@ -8,6 +8,10 @@
     python -m streaming_causal_video_timestep_b200.microbench gemm_fp8 [--iters N]
     python -m streaming_causal_video_timestep_b200.microbench attn_fp8 [--iters N]
     python -m streaming_causal_video_timestep_b200.microbench qkv_stream [--iters N] [--fp8]
+    python -m streaming_causal_video_timestep_b200.microbench rope_axes [--iters N]
+    python -m streaming_causal_video_timestep_b200.microbench cache_append [--iters N]
+    python -m streaming_causal_video_timestep_b200.microbench attn_cache [--iters N]
+    python -m streaming_causal_video_timestep_b200.microbench attn_cache_token [--iters N]
 
 attn : one block's attention in steady state at the 14B-like shape: 4680
        queries x 40 heads x 128 over [sink 1560 | 2 window blocks | block]
@@ -28,6 +32,11 @@ qkv_stream: the QKV projection with its fused RoPE / ring-append epilogue and
        4-slot grouped stream ([18720, 5120] x [15360, 5120]^T and x [5120,
        5120]^T), in a one-sublayer stream at the 14B-like shape; bf16, or with
        --fp8 on e4m3 operands; timed by the stream's profiling counters.
+rope_axes: rotary positions of one block's q and k, 4680 tokens x 80 heads x 128 bf16
+       on (time, height, width), 192 MB read and written.
+cache_append: the same block's K (rotated) and V into a paged e4m3 cache (pages of 64).
+attn_cache: attention of one block over [sink | 2 window blocks | block] as attn, on that
+       cache; attn_cache_token: one query token of each of 16 streams over 14040 keys.
 Inputs exceed L2 (126 MB) except the per-slot attention keys (160 MB K/V +
 48 MB q).  Each timed loop spans at least 1.5 s; prints one JSON line per mode
 with the SM clock record (median under load, throttle reasons) taken around it.
@@ -40,7 +49,8 @@ import json
 import torch
 
 from .clocks import ClockSampler
-from .stream import op_attention, op_attention_fp8, op_euler, op_gemm, op_gemm_fp8, op_quantize_e4m3
+from .stream import (op_attention, op_attention_cache_fp8, op_attention_fp8, op_cache_append_fp8, op_euler, op_gemm,
+                     op_gemm_fp8, op_quantize_e4m3, op_rope_axes)
 
 
 def _time(fn, iters, warmup=3, min_ms=1500.0):
@@ -241,21 +251,90 @@ def bench_qkv_stream(iters, fp8=False):
     return res
 
 
+def _grid_positions(n):
+    i = torch.arange(n, device="cuda")
+    return torch.stack([i // 1560, i % 1560 // 52, i % 52], 1).to(torch.int32)
+
+
+def _int32(*values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _cache(batch, keys, heads=40, page=64, d=128):
+    """An empty paged cache for `keys` tokens of each of `batch` sequences."""
+    width = -(-keys // page)
+    pages = [torch.zeros((batch * width, heads, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones((batch * width, heads), device="cuda") for _ in range(2)]
+    table = torch.randperm(batch * width, device="cuda").to(torch.int32).view(batch, width)
+    return (*pages, *scales, table)
+
+
+def bench_rope_axes(iters):
+    T, H, d = 4680, 80, 128
+    x = torch.randn(T, H, d, device="cuda").to(torch.bfloat16)
+    out, pos = torch.empty_like(x), _grid_positions(T)
+    ms = _time(lambda: op_rope_axes(x, pos, (22, 21, 21), out=out), iters)
+    nbytes = 2 * T * H * d * 2 + T * 12
+    return {"mode": "rope_axes", "shape": f"{T}x{H}x{d} bf16, 3 axes", "ms": round(ms, 4),
+            "gbs": round(nbytes / ms / 1e6, 1), "bytes": nbytes}
+
+
+def bench_cache_append(iters):
+    T, H, d = 4680, 40, 128
+    k, v = (torch.randn(T, H, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache, pos, lens, cu = _cache(1, T), _grid_positions(T), _int32(0), _int32(0, T)
+    ms = _time(lambda: op_cache_append_fp8(k, v, *cache, lens, cu, T, pos=pos, pairs=(22, 21, 21)), iters)
+    nbytes = 2 * T * H * d * 3 + T * 12 + 2 * cache[2].numel() * 4
+    return {"mode": "cache_append", "shape": f"{T}x{H}x{d} bf16 to e4m3 pages of 64", "ms": round(ms, 4),
+            "gbs": round(nbytes / ms / 1e6, 1), "bytes": nbytes}
+
+
+def _filled(batch, keys, heads=40, d=128):
+    cache = _cache(batch, keys, heads, d=d)
+    for b in range(batch):
+        k, v = (torch.randn(keys, heads, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+        op_cache_append_fp8(k, v, *cache[:4], cache[4][b:b + 1].contiguous(), _int32(0), _int32(0, keys), keys)
+    return cache
+
+
+def bench_attn_cache(iters):
+    H, d, T, N = 40, 128, 4680, 15600
+    q, cache = torch.randn(T, H, d, device="cuda").to(torch.bfloat16), _filled(1, N)
+    out, kv, cu = torch.empty_like(q), _int32(N), _int32(0, T)
+    ms = _time(lambda: op_attention_cache_fp8(q, *cache, kv, cu, T, N, out=out), iters)
+    flops = 4.0 * T * N * d * H
+    return {"mode": "attn_cache", "shape": f"{T} q x {N} keys x {H}x{d}, e4m3 pages of 64", "ms": round(ms, 4),
+            "tflops": round(flops / ms / 1e9, 1), "flops": flops}
+
+
+def bench_attn_cache_token(iters):
+    B, H, d, N = 16, 40, 128, 14040
+    q, cache = torch.randn(B, H, d, device="cuda").to(torch.bfloat16), _filled(B, N)
+    out, kv, cu = torch.empty_like(q), _int32(*[N] * B), _int32(*range(B + 1))
+    ms = _time(lambda: op_attention_cache_fp8(q, *cache, kv, cu, 1, N, out=out, causal_block=1), iters)
+    nbytes = 2 * B * N * H * d + 4 * B * H * d
+    return {"mode": "attn_cache_token", "shape": f"{B} x 1 q x {N} keys x {H}x{d}, e4m3 pages of 64", "ms": round(ms, 4),
+            "gbs": round(nbytes / ms / 1e6, 1), "bytes": nbytes}
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("mode", choices=["attn", "attn_fp8", "gemm", "gemm_out", "euler", "rerope", "gemm_fp8",
-                                     "qkv_stream", "all"])
+                                     "qkv_stream", "rope_axes", "cache_append", "attn_cache", "attn_cache_token", "all"])
     ap.add_argument("--iters", type=int, default=10)
     ap.add_argument("--layers", type=int, default=8, help="rerope: sublayers of the stream (one launch covers all)")
     ap.add_argument("--fp8", action="store_true", help="qkv_stream: e4m3 projections")
     args = ap.parse_args()
-    modes = ["attn", "attn_fp8", "gemm", "gemm_out", "gemm_fp8", "euler", "rerope"] if args.mode == "all" else [args.mode]
+    modes = ["attn", "attn_fp8", "gemm", "gemm_out", "gemm_fp8", "euler", "rerope", "rope_axes", "cache_append",
+             "attn_cache", "attn_cache_token"] if args.mode == "all" else [args.mode]
     for m in modes:
         clocks = ClockSampler(torch.cuda.current_device())
         clocks.start()
         r = {"attn": bench_attn, "attn_fp8": bench_attn_fp8, "gemm": bench_gemm, "gemm_out": bench_gemm_out,
              "euler": bench_euler, "rerope": lambda it: bench_rerope(it, args.layers),
-             "gemm_fp8": bench_gemm_fp8, "qkv_stream": lambda it: bench_qkv_stream(it, args.fp8)}[m](args.iters)
+             "gemm_fp8": bench_gemm_fp8, "qkv_stream": lambda it: bench_qkv_stream(it, args.fp8),
+             "rope_axes": bench_rope_axes, "cache_append": bench_cache_append, "attn_cache": bench_attn_cache,
+             "attn_cache_token": bench_attn_cache_token}[m](args.iters)
         r["clocks"] = clocks.stop()
         print(json.dumps(r), flush=True)
 

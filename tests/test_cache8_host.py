@@ -112,7 +112,7 @@ def _rope(lib, dtype=0, x=BUF, xt=128, xh=64, out=BUF, ot=128, oh=64, tokens=1, 
     dict(heads=65536, xt=1 << 30, ot=1 << 30), dict(d=0), dict(d=1), dict(d=257), dict(pairs=()), dict(pairs=(0, 0)),
     dict(pairs=(33,)), dict(pairs=(12, 10, 11)), dict(pairs=(-1, 3)), dict(pairs=(1, 1, 1, 1, 1)), dict(theta=0.5),
     dict(theta=float("nan")), dict(theta=float("inf")), dict(xh=63), dict(oh=0), dict(xt=-1), dict(ot=0, tokens=2),
-    dict(x=BUF + 1), dict(out=BUF + 1), dict(pos=BUF + 2), dict(dtype=1, x=BUF + 2), dict(naxes=-1),
+    dict(ot=64, tokens=3), dict(ot=100, tokens=2, oh=64), dict(x=BUF + 1), dict(out=BUF + 1), dict(pos=BUF + 2), dict(dtype=1, x=BUF + 2), dict(naxes=-1),
 ])
 def test_rope_axes_refuses(lib, over):
     assert _rope(lib, **over) == _lib.LA_EINVAL
@@ -169,7 +169,7 @@ def _attn(lib, dtype=0, q=BUF, qt=256, qh=64, tokens=2, q_heads=4, cu=BUF, lens=
 @pytest.mark.parametrize("over", CACHE_BAD + [
     dict(dtype=1), dict(dtype=3), dict(q=None), dict(out=None), dict(cu=None), dict(lens=None), dict(tokens=-1), dict(q_heads=3),
     dict(q_heads=0), dict(max_q=-1), dict(max_kv=-1), dict(causal=-1), dict(scale=0.0), dict(scale=-1.0),
-    dict(scale=float("nan")), dict(scale=float("inf")), dict(qh=63), dict(qt=-1), dict(ot=0), dict(oh=66), dict(ot=258),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(qh=63), dict(qt=-1), dict(ot=0), dict(ot=64, oh=64), dict(ot=128, oh=64), dict(oh=66), dict(ot=258),
     dict(out=BUF + 4), dict(q=BUF + 1), dict(out32=BUF + 8), dict(max_kv=1 << 20, ws_bytes=0), dict(max_kv=1 << 20, ws=None),
     dict(max_kv=1 << 20, ws=BUF + 8),
 ])

@@ -543,3 +543,12 @@ def test_stream_argument_and_device_checks():
     op_rope_axes(x, pos, PAIRS[64], out=out, stream=side)
     side.synchronize()
     assert torch.equal(out, ref)
+
+
+def test_microbenchmarks_run(monkeypatch):
+    from streaming_causal_video_timestep_b200 import microbench
+    monkeypatch.setattr(microbench, "_time", lambda fn, iters: (fn(), torch.cuda.synchronize(), 1.0)[2])
+    for f in (microbench.bench_rope_axes, microbench.bench_cache_append, microbench.bench_attn_cache,
+              microbench.bench_attn_cache_token):
+        r = f(1)
+        assert r["mode"] and (r.get("bytes") or r.get("flops")) > 0
