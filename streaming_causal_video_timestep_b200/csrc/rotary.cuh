@@ -3,7 +3,7 @@
 // Pair j (of n) turns by pos[axis(j)] * omega_j.  The angle is kept in turns as a
 // 64-bit fixed-point fraction: omega_j / (2 pi) * 2^64 is rounded once on the host
 // and the product with the (signed) position wraps modulo 2^64, which is exactly
-// "modulo one turn".  Its error is |pos| * 2^-62 turns at most, for every position an
+// "modulo one turn".  Its error is |pos| * 2^-61 turns at most, for every position an
 // int32 holds, where pos * omega in fp32 would lose 2^-24 * pos * omega radians (6e-3
 // at position 1e5).  Its top 32 bits, as an integer, give the quadrant and the signed
 // rest within an eighth of a turn exactly; the rest goes to fp32 once and into the

@@ -332,7 +332,7 @@ _HALVES = {torch.bfloat16: _lib.LA_BF16, torch.float16: _lib.LA_FP16}
 def _rows(t, name, dev=None, dtypes=_FLOATS):
     """Checks a [tokens, heads, head_dim] tensor with contiguous head_dim; returns (pointer, token and head strides).
     dev: the index of the device that it has to be on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0 or t.dim() != 3:
         raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, head_dim]")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
@@ -346,12 +346,13 @@ def _rows(t, name, dev=None, dtypes=_FLOATS):
 
 def _dense(t, dtype, shape, name, dev):
     """Checks a contiguous tensor on CUDA device `dev` (an index); returns its pointer."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor):
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+        if t.is_cuda:
+            raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    raise TypeError(f"{name} must be a CUDA tensor")
 
 
 def _call(fn, dev, stream, *args):
@@ -395,7 +396,7 @@ def _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev):
 
 def _like(x, out, name="out"):
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{name}: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
     return out
@@ -473,10 +474,10 @@ def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, k
     ws = None
     if need > 0:
         if stream is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = q.new_empty(need // 2)
         else:
             with torch.cuda.stream(stream):     # the allocator hands it out again behind that stream's work
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+                ws = q.new_empty(need // 2)
     _call(lib.la_op_attention_cache_fp8, dev, stream, ref, _HALVES[q.dtype], pq, qt, qh, tokens, heads, pcu, plen, max_q,
           max_kv, causal_block, d ** -0.5 if scale is None else scale, po, ot, oh, p32, None if ws is None else ws.data_ptr(),
           need)
