@@ -63,10 +63,12 @@ template <typename T, int D, int PAGE> struct Ring {
   static constexpr int STAGES = STAGE <= 16384 ? 4 : STAGE <= 32768 ? 3 : 2;
 };
 
-// A thread owns 8 pairs of one token a pass: pairs 8u .. 8u+7 of its row, D/16
-// threads a row.  VEC: the pairs' elements are 16-byte vectors of the input and 16
-// (or twice 8) consecutive codes.
-// HALF: tab.half.
+// A thread owns 16 elements of one token a pass, D/16 threads a row.  VEC: as 16-byte
+// vectors, the w-th of thread u at element w * N * D/16 + N * u, so that a row's threads
+// read and write next to each other (vectors that lie side by side in a thread fetch
+// every 32-byte sector twice), and both elements of a pair are the thread's own: pairs
+// lie in a vector, or (HALF: tab.half over all of a row) in vectors half a row apart.
+// Not VEC: pairs 8u .. 8u+7.
 template <typename T, int D, int PAGE, bool VEC, bool HALF>
 __global__ void __launch_bounds__((Ring<T, D, PAGE>::THREADS))
 k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constant__ RotaryTable tab) {
@@ -104,13 +106,10 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
   const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.heads);
   const T* x = static_cast<const T*>(is_v ? p.v : p.k);
   const long long st = is_v ? p.v_st : p.k_st, sh = is_v ? p.v_sh : p.k_sh;
-  const bool half = HALF && !is_v && 8 * u < tab.n;   // this thread's pairs lie n apart
   extern __shared__ __align__(16) uint8_t ring_raw[];
   uint4* ring = reinterpret_cast<uint4*>(ring_raw);
-  // Row base of this thread's elements (+ hi for the second vector) at the next head to
-  // fetch, and the stage it goes to.
-  const T* src = x + (tok0 + row) * st + h0 * sh + (half ? 8 * u : 16 * u);
-  const int hi = half ? tab.n : 8;
+  // This thread's first vector of the next head to fetch, and the stage it goes to.
+  const T* src = x + (tok0 + row) * st + h0 * sh + N * u;
   int into = 0;
   auto fetch = [&](int h) {
     if constexpr (VEC) {
@@ -121,10 +120,7 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
           if (row + i * ROWS < cnt) {
             const T* xr = src + i * ROWS * st;
 #pragma unroll
-            for (int w = 0; w < 8 / N; ++w) {
-              cp_async16(to + (i * R::PER + w) * THREADS, xr + w * N);
-              cp_async16(to + (i * R::PER + 8 / N + w) * THREADS, xr + hi + w * N);
-            }
+            for (int w = 0; w < R::PER; ++w) cp_async16(to + (i * R::PER + w) * THREADS, xr + w * (N * TPR));
           }
         }
         src += sh;
@@ -145,8 +141,12 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
     for (int i = 0; i < NP; ++i) {
       const int r = row + i * ROWS;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        cs[i][k] = r < cnt && 8 * u + k < tab.n ? pairs.cos_sin_nearest(8 * u + k, p.pos + (tok0 + r) * tab.naxes) : make_float2(1.f, 0.f);
+      for (int k = 0; k < 8; ++k) {
+        int j = 8 * u + k;                          // the pair of f[2k], f[2k+1]
+        if (VEC && HALF) j = k / N * (N * TPR) + N * u + k % N;               // of f[k], f[k+8]
+        else if (VEC) j = (2 * k / N * (N * TPR) + N * u + 2 * k % N) / 2;
+        cs[i][k] = r < cnt && j < tab.n ? pairs.cos_sin_nearest(j, p.pos + (tok0 + r) * tab.naxes) : make_float2(1.f, 0.f);
+      }
     }
   }
   // The warps' maxima of a head, in turn in one of two rows: a row is written again only
@@ -166,23 +166,15 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
     }
     const uint4* from = ring + stage * (R::STAGE / 16) + threadIdx.x;
     stage = stage + 1 == R::STAGES ? 0 : stage + 1;
-    float f[NP][16];                                // pair k of the 8: f[2k], f[2k+1]
+    float f[NP][16];
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = row + i * ROWS;
       if (r < cnt) {
         if constexpr (VEC) {
-          float a[16];
 #pragma unroll
-          for (int w = 0; w < R::PER; ++w) Vec16<T>::unpack(from[(i * R::PER + w) * THREADS], a + w * N);
-          if (half) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) f[i][k] = a[k / 2 + (k & 1) * 8];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) f[i][k] = a[k];
-          }
+          for (int w = 0; w < R::PER; ++w) Vec16<T>::unpack(from[(i * R::PER + w) * THREADS], f[i] + w * N);
         } else {
           const T* xr = x + (tok0 + r) * st + h * sh;
 #pragma unroll
@@ -195,9 +187,11 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
         if (rotate) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float v = f[i][2 * k], w = f[i][2 * k + 1];
-            f[i][2 * k] = __fsub_rn(__fmul_rn(v, cs[i][k].x), __fmul_rn(w, cs[i][k].y));
-            f[i][2 * k + 1] = __fadd_rn(__fmul_rn(v, cs[i][k].y), __fmul_rn(w, cs[i][k].x));
+            float& a = f[i][VEC && HALF ? k : 2 * k];
+            float& b = f[i][VEC && HALF ? k + 8 : 2 * k + 1];
+            const float v = a, w = b;
+            a = __fsub_rn(__fmul_rn(v, cs[i][k].x), __fmul_rn(w, cs[i][k].y));
+            b = __fadd_rn(__fmul_rn(v, cs[i][k].y), __fmul_rn(w, cs[i][k].x));
           }
         }
 #pragma unroll
@@ -214,7 +208,9 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
     if (off0) s = (old != old || s != s) ? __uint_as_float(0x7fc00000u) : fmaxf(old, s);
     const bool fine = s == s;
     // 1 / s, a power of two; 0 for the NaN, whose page gets zeros
-    const float inv = fine ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+    // (a scale of another kind can only be the caller's own, from before)
+    float inv = fine ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+    if (fine && (__float_as_uint(s) & 0x7fffffu)) inv = 1.0f / s;
     if (off0 && fine && s != old) {                 // the page's older codes follow the scale
       const float g = old * inv;
       for (int q = threadIdx.x; q < off0 * (D / 8); q += THREADS) {
@@ -234,23 +230,17 @@ k_cache_append(const __grid_constant__ CacheAppendParams p, const __grid_constan
         if constexpr (VEC) {
           const float2 ii = make_float2(inv, inv);
           uint32_t w[4];
-          if (half) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float* a = f[i] + 8 * (q & 1) + (q >> 1);
-              w[q] = pack_e4m3x4(__fmul2_rn(make_float2(a[0], a[2]), ii), __fmul2_rn(make_float2(a[4], a[6]), ii));
-            }
-            if (!fine) w[0] = w[1] = w[2] = w[3] = 0;
-            *reinterpret_cast<uint2*>(cr + 8 * u) = make_uint2(w[0], w[1]);
-            *reinterpret_cast<uint2*>(cr + tab.n + 8 * u) = make_uint2(w[2], w[3]);
-          } else {
+          for (int q = 0; q < 4; ++q) {
+            const float* a = f[i] + 4 * q;
+            w[q] = pack_e4m3x4(__fmul2_rn(make_float2(a[0], a[1]), ii), __fmul2_rn(make_float2(a[2], a[3]), ii));
+          }
+          if (!fine) w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float* a = f[i] + 4 * q;
-              w[q] = pack_e4m3x4(__fmul2_rn(make_float2(a[0], a[1]), ii), __fmul2_rn(make_float2(a[2], a[3]), ii));
-            }
-            if (!fine) w[0] = w[1] = w[2] = w[3] = 0;
-            *reinterpret_cast<uint4*>(cr + 16 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int v = 0; v < R::PER; ++v) {
+            uint8_t* to = cr + v * (N * TPR) + N * u;
+            if constexpr (N == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[2 * v], w[2 * v + 1]);
+            else *reinterpret_cast<uint32_t*>(to) = w[v];
           }
         } else {
 #pragma unroll
@@ -272,8 +262,7 @@ cudaError_t launch(CacheAppendParams p, const RotaryTable& tab, int num_sms, cud
   auto ok16 = [](const void* q, long long a, long long b) {
     return reinterpret_cast<uintptr_t>(q) % 16 == 0 && a * sizeof(T) % 16 == 0 && b * sizeof(T) % 16 == 0;
   };
-  // Halves: a thread's 8 pairs are either all rotated or all passed through.
-  const bool vec = (!tab.half || tab.n % 8 == 0) && ok16(p.k, p.k_st, p.k_sh) && ok16(p.v, p.v_st, p.v_sh);
+  const bool vec = (!tab.half || 2 * tab.n == D) && ok16(p.k, p.k_st, p.k_sh) && ok16(p.v, p.v_st, p.v_sh);
   p.pages_per_seq = (p.max_new + PAGE - 1) / PAGE + 1;
   const long long gx = static_cast<long long>(p.batch) * p.pages_per_seq;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;

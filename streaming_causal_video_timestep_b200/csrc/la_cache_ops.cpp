@@ -32,7 +32,7 @@ bool fill_table(RotaryTable& t, int32_t d, int32_t naxes, const int32_t* pairs, 
                 int32_t inverse) {
   t.n = 0;
   t.naxes = naxes;
-  t.half = half != 0;
+  t.half = half != 0 && naxes > 0;
   t.inverse = inverse != 0;
   if (naxes < 0 || naxes > LA_MAX_AXES || (naxes > 0 && !pairs)) return false;
   if (naxes > 0 && !(theta >= 1.0 && theta <= 1e12)) return false;
