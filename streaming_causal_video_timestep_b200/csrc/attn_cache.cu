@@ -64,6 +64,16 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
   const int b = blockIdx.z, hk = blockIdx.y;
   const int split = blockIdx.x % p.nsplit, tile = blockIdx.x / p.nsplit;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, n = lane >> 2, c = lane & 3;
+  // Pieces are of the same length for every sequence, set by the call's bound of the
+  // keys (the last takes what is left), so the first table entries are read beside the
+  // sequence's lengths.
+  const int s0 = split * p.piece_steps;
+  int early[STAGES];
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) {
+    const int at = (s0 + warp + i * WARPS) * 16 >> p.page_shift;
+    early[i] = at < p.max_pages ? __ldg(p.block_table + static_cast<long long>(b) * p.max_pages + at) : -1;
+  }
   const CacheSeq s = cache_seq(p, b);
   if (s.bad && blockIdx.x == 0 && hk == 0 && threadIdx.x == 0) raise_device_error(p.err, LA_DEVERR_BAD_DESC);
   const int G = p.heads / p.kv_heads;
@@ -73,8 +83,7 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
   const int last = min(rows, r0 + 16) - 1;
   const int keys = cache_limit(p, s, last / G);                 // limits do not fall along the rows
   const int steps = (keys + 15) / 16;
-  const int per = (steps + p.nsplit - 1) / p.nsplit;
-  const int s0 = split * per, s1 = min(steps, s0 + per);
+  const int s1 = split == p.nsplit - 1 ? steps : min(steps, s0 + p.piece_steps);
 
   // The first steps' copies are under way while Q is brought in.
   extern __shared__ __align__(16) uint8_t ring_raw[];
@@ -99,9 +108,10 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");     // one group a step, empty ones too
   };
-  int st = s0 + warp, pg = page_of(st);
+  int st = s0 + warp, pg = st < s1 ? cache_page_checked(p, early[0]) : -1;
+#pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
-    const int nx = page_of(st + (i + 1) * WARPS);
+    const int nx = st + (i + 1) * WARPS < s1 ? cache_page_checked(p, early[i + 1]) : -1;
     fetch(st + i * WARPS, pg, i);
     pg = nx;
   }

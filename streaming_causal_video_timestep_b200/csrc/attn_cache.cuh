@@ -51,12 +51,15 @@ __device__ __forceinline__ CacheUnit cache_unit(const AttnCacheParams& p, int un
   const int bh = unit / p.pairs;
   return {bh / p.kv_heads, bh % p.kv_heads, p.pairs - 1 - unit % p.pairs};
 }
-// Page of the sequence that holds key j (j < L), -1 (and the error word) if the table names none.
-__device__ __forceinline__ int cache_page(const AttnCacheParams& p, int b, int j) {
-  const int pg = p.block_table[static_cast<long long>(b) * p.max_pages + (j >> p.page_shift)];
+// A page that the table names, -1 (and the error word) if there is no such page.
+__device__ __forceinline__ int cache_page_checked(const AttnCacheParams& p, int pg) {
   if (pg >= 0 && pg < p.num_pages) return pg;
   raise_device_error(p.err, LA_DEVERR_BAD_DESC);
   return -1;
+}
+// Page of the sequence that holds key j (j < L).
+__device__ __forceinline__ int cache_page(const AttnCacheParams& p, int b, int j) {
+  return cache_page_checked(p, p.block_table[static_cast<long long>(b) * p.max_pages + (j >> p.page_shift)]);
 }
 
 // Two e4m3 codes (low 16 bits) to fp16, exactly.

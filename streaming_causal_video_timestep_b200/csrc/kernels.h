@@ -182,7 +182,7 @@ struct AttnCacheParams {
   // Few rows: every row's keys in nsplit pieces, part_* [nsplit, batch, max_q, heads] rows.
   // Many rows: units of 256 rows of a (sequence, key head), pairs of them each; the first
   // `full` whole, the others in nsplit pieces, part_* [nsplit, (units - full) * 256] rows.
-  int nsplit, pairs, full, units;
+  int nsplit, piece_steps, pairs, full, units;   // piece_steps (few rows): 16 keys each
   float* part_o; float2* part_ml;      // nsplit > 1: a row's d sums, and (maximum, normaliser)
   int* err;
 };

@@ -245,6 +245,7 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
   Plan pl;
   if (!plan_call(pl, p.max_q, max_kv, p.batch, heads, cache->heads)) return LA_EINVAL;
   p.nsplit = pl.nsplit;
+  p.piece_steps = static_cast<int>(((max_kv + 15) / 16 + p.nsplit - 1) / p.nsplit);
   p.pairs = pl.pairs;
   p.full = pl.full;
   p.units = pl.units;
