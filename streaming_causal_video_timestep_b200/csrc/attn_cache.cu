@@ -32,7 +32,7 @@ constexpr int WARPS = 4;
 constexpr int STAGES = 4;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -57,7 +57,10 @@ template <int D> constexpr size_t rows_smem() {
   return ring > join ? ring : join;
 }
 
-template <typename T, int D>
+// HALVES: 8-row halves of the MMA's 16 rows that hold rows of this call; an empty half
+// costs its part of the softmax otherwise (at 1 row, 16 x 40 heads over up to 14040 keys:
+// 258 us, 270 with both).
+template <typename T, int D, int HALVES>
 __global__ void __launch_bounds__(WARPS * 32, 3)
 k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
   if (p.nsplit > 1) launch_dependents();    // the join may take its place; it waits for this grid's end
@@ -83,6 +86,7 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
   const int last = min(rows, r0 + 16) - 1;
   const int keys = cache_limit(p, s, last / G);                 // limits do not fall along the rows
   const int steps = (keys + 15) / 16;
+  const int low = cache_limit(p, s, r0 / G);                    // and the tile's first row has the least
   const int s1 = split == p.nsplit - 1 ? steps : min(steps, s0 + p.piece_steps);
 
   // The first steps' copies are under way while Q is brought in.
@@ -190,22 +194,29 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     }
     // x[nt][2 i + e]: row n + 8 i, key 8 nt + ((2 c + e) ^ 4 e)
     const float lv = __log2f(vs), rv = __frcp_rn(vs);
-    float mt[2];
+    float mt[HALVES];
+    const bool full = st * 16 + 16 <= low;                   // no row of the tile is masked here
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < HALVES; ++i) {
       const float a = sc[i] * ks;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = st * 16 + nt * 8 + ((2 * c + e) ^ e << 2);
-          x[nt][2 * i + e] = key < lim[i] ? fmaf(x[nt][2 * i + e], a, lv) : -INFINITY;
-        }
+        for (int e = 0; e < 2; ++e) x[nt][2 * i + e] = fmaf(x[nt][2 * i + e], a, lv);
+      if (!full) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (st * 16 + nt * 8 + ((2 * c + e) ^ e << 2) >= lim[i]) x[nt][2 * i + e] = -INFINITY;
+      }
       mt[i] = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
     }
-    if (__any_sync(0xffffffffu, mt[0] > m[0] + LA_CACHE_P_TAU || mt[1] > m[1] + LA_CACHE_P_TAU)) {
+    bool need = mt[0] > m[0] + LA_CACHE_P_TAU;
+    if (HALVES == 2) need = need || mt[HALVES - 1] > m[HALVES - 1] + LA_CACHE_P_TAU;
+    if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < HALVES; ++i) {
         float t = mt[i];
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
@@ -220,9 +231,9 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
         }
       }
     }
-    uint32_t pa[4];
+    uint32_t pa[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < HALVES; ++i) {
       const float off = LA_CACHE_P_BIAS - (m[i] == -INFINITY ? 0.f : m[i]);
       float e[4];
 #pragma unroll
@@ -387,7 +398,7 @@ cudaError_t launch_rows(const AttnCacheParams& p, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.max_q) * (p.heads / p.kv_heads);
   const long long gx = (rows + 15) / 16 * p.nsplit;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidValue;
-  auto kern = k_attn_cache_rows<T, D>;
+  auto kern = rows <= 8 ? k_attn_cache_rows<T, D, 1> : k_attn_cache_rows<T, D, 2>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(rows_smem<D>()));
   if (e != cudaSuccess) return e;
   kern<<<dim3(static_cast<unsigned>(gx), p.kv_heads, p.batch), WARPS * 32, rows_smem<D>(), st>>>(p);
