@@ -41,6 +41,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
@@ -102,11 +105,22 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
       const long long at = plane * (p.page_tokens * D) + (st * 16 & (p.page_tokens - 1)) * D;
       const int valid = on ? keys - st * 16 : 0;             // rows behind the last key become zeros
       Step<D>& x = ring[slot];
+      const uint8_t* kp = p.k_pages + at + lane * 16;
+      const uint8_t* vp = p.v_pages + at + lane * 16;
+      if (valid >= 16) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int q = i * 32 + lane, r = q / (D / 16), ch = q % (D / 16);
-        cp_async16(x.k + slot_of<D>(r, ch), p.k_pages + at + q * 16, r < valid);
-        cp_async16(x.v + slot_of<D>(r, ch), p.v_pages + at + q * 16, r < valid);
+        for (int i = 0; i < D / 32; ++i) {
+          const int q = i * 32 + lane, to = slot_of<D>(q / (D / 16), q % (D / 16));
+          cp_async16(x.k + to, kp + i * 512);
+          cp_async16(x.v + to, vp + i * 512);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int q = i * 32 + lane, r = q / (D / 16), to = slot_of<D>(r, q % (D / 16));
+          cp_async16(x.k + to, kp + i * 512, r < valid);
+          cp_async16(x.v + to, vp + i * 512, r < valid);
+        }
       }
       if (lane < 2) cp_async4(lane ? &scales[warp][slot].y : &scales[warp][slot].x, (lane ? p.v_scale : p.k_scale) + plane, on);
     }
