@@ -370,7 +370,9 @@ SHAPES = [  # batch lens of keys, queries, key heads, group, page, d, causal
     ([1000, 333], [1, 1], 3, 1, 64, 128, 0), ([4097], [1], 1, 8, 128, 64, 1), ([700, 65, 64], [3, 5, 1], 2, 5, 64, 128, 1),
     ([129, 40], [16, 7], 1, 1, 32, 128, 1), ([300], [130], 2, 2, 64, 128, 1), ([257, 0, 31], [200, 5, 31], 2, 1, 32, 64, 7),
     ([390], [257], 1, 3, 128, 128, 0), ([50, 128], [64, 300], 1, 2, 64, 64, 1), ([512], [256], 2, 1, 64, 128, 128),
-    ([1300], [513], 1, 2, 128, 64, 100), ([64, 640], [0, 384], 2, 1, 64, 128, 192),
+    ([1300], [513], 1, 2, 128, 64, 100), ([64, 640], [0, 384], 2, 1, 64, 128, 192), ([33, 70], [17, 16], 2, 1, 32, 64, 1),
+    ([200], [5], 1, 3, 64, 64, 2), ([96, 97, 95], [2, 1, 2], 1, 8, 32, 128, 1), ([128], [128], 1, 2, 128, 128, 1),
+    ([140], [129], 1, 2, 64, 128, 1000), ([2, 1], [300, 20], 1, 1, 64, 128, 3),
 ]
 
 
@@ -393,6 +395,23 @@ def test_attention_split_long_keys(nq):
     near(np64(a), np64(b), np.abs(np64(b)) * 2.0 ** -7 + 2.0 ** -12 * 8)       # two bf16 roundings of values 2^-11 (a <= 8) apart
     for _ in range(3):
         assert torch.equal(attend(c, q, [9000], [0, nq], 1)[0], a)             # the same bits every time
+
+
+@pytest.mark.parametrize("nq,max_kv", [(1, 3000), (1, 10 ** 6), (8, 700), (150, 2000), (150, 10 ** 6)])
+def test_attention_whatever_the_bound_says(nq, max_kv):
+    """max_kv below the length (the last piece takes the rest) and far above it (most pieces are empty)."""
+    c = filled(26, 2, [5000, 90], 1, 32, 64)
+    check_attention(c, rand(32, 2 * nq, 2, 64), [5000, 90], [0, nq, 2 * nq], 1, max_kv=max_kv)
+
+
+def test_attention_rows_of_no_sequence():
+    """A buffer much longer than the batch: its other rows are left alone and cost no workspace."""
+    from streaming_causal_video_timestep_b200 import load
+    c = filled(27, 1, [3000], 1, 64, 64)
+    q = rand(33, 5000, 1, 64)
+    out = torch.full_like(q, 3.0)
+    check_attention(c, q, [3000], [0, 1], 1, out=out)
+    assert (out[1:] == 3).all() and load() is not None
 
 
 @pytest.mark.parametrize("nq,G", [(1, 1), (1, 4), (40, 2)])
@@ -437,17 +456,20 @@ def test_attention_does_not_see_what_is_masked(nq):
     assert got[first:].isnan().all() and torch.equal(got[:first], ref[:first])
 
 
-def test_attention_strides_and_out():
+@pytest.mark.parametrize("n", [30, 3])
+def test_attention_strides_and_out(n):
     c = filled(24, 1, [200], 2, 64, 128)
-    qkv = rand(5, 30, 8, 128)
-    ref = attend(c, qkv[:, :4].contiguous(), [200], [0, 30], 1)[0]
-    assert torch.equal(attend(c, qkv[:, :4], [200], [0, 30], 1)[0], ref)
+    qkv = rand(5, n, 8, 128)
+    ref = attend(c, qkv[:, :4].contiguous(), [200], [0, n], 1)[0]
+    assert torch.equal(attend(c, qkv[:, :4], [200], [0, n], 1)[0], ref)
     planes = qkv[:, :4].transpose(0, 1).contiguous().transpose(0, 1)
-    assert torch.equal(attend(c, planes, [200], [0, 30], 1)[0], ref)
-    odd = torch.zeros(30, 4, 131, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(attend(c, planes, [200], [0, n], 1)[0], ref)
+    odd = torch.zeros(n, 4, 131, dtype=torch.bfloat16, device="cuda")
     odd[..., 3:] = qkv[:, :4]
-    out = torch.full((30, 4, 136), 5.0, dtype=torch.bfloat16, device="cuda")
-    attend(c, odd[..., 3:], [200], [0, 30], 1, out=out[..., 4:132])
+    out = torch.full((n, 4, 136), 5.0, dtype=torch.bfloat16, device="cuda")
+    attend(c, odd[..., 3:], [200], [0, n], 1, out=out[..., 4:132])
+    own = qkv[:, :4].clone()
+    assert attend(c, own, [200], [0, n], 1, out=own)[0] is own and torch.equal(own, ref)      # over its own queries
     assert torch.equal(out[..., 4:132], ref) and (out[..., :4] == 5).all() and (out[..., 132:] == 5).all()
 
 
@@ -470,6 +492,37 @@ def test_attention_reports_what_does_not_fit():
             assert status() == _lib.LA_EDEVICE and status() == _lib.LA_OK
             assert torch.equal(out[:nq], good[:nq]) and torch.equal(out[2 * nq:], good[2 * nq:]) and out.isfinite().all()
         c.g[4][1, 0] = keep
+
+
+def test_offsets_past_32_bits():
+    """Pages whose codes lie beyond 4 GiB of the cache, and rotary rows beyond 2^31 elements."""
+    from streaming_causal_video_timestep_b200 import op_attention_cache_fp8, op_cache_append_fp8, op_rope_axes
+    H, page, d, L = 8, 128, 128, 300
+    num = (1 << 32) // (H * page * d) + 40
+    big = [torch.empty((num, H, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones((num, H), device="cuda") for _ in range(2)]
+    table = i32([[num - 1, num - 7, num - 20]])
+    small = Cache(41, 1, 3, H, page, d, spare=0)
+    k, v = rand(42, L, H, d), rand(43, L, H, d)
+    small.append(k, v, [0], [0, L])
+    op_cache_append_fp8(k, v, *big, *scales, table, i32([0]), i32([0, L]), L)
+    for j in range(3):
+        rows = min(page, L - j * page)
+        for a, b in zip(big, small.g[:2]):
+            assert torch.equal(a[table[0, j]][:, :rows], b[small.table[0, j]][:, :rows])
+    for n in (1, 200):
+        q = rand(44, n, H, d)
+        args = i32([L]), i32([0, n]), n, L
+        assert torch.equal(op_attention_cache_fp8(q, *big, *scales, table, *args, causal_block=1),
+                           op_attention_cache_fp8(q, *small.g, *args, causal_block=1))
+    del big
+    T, H = (1 << 31) // (64 * 128) + 5, 64
+    x = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rand(45, 3, H, d)
+    pos = torch.zeros(T, 3, dtype=torch.int32, device="cuda")
+    pos[-3:] = i32([[5, 6, 7], [8, 9, 10], [11, 12, 13]])
+    y = op_rope_axes(x, pos, PAIRS[d])
+    assert torch.equal(y[-3:], op_rope_axes(x[-3:].clone(), pos[-3:].clone(), PAIRS[d])) and not y[:-3].any()
 
 
 # ---- together ----------------------------------------------------------------------------------------
