@@ -63,7 +63,9 @@ bool rows_apart(int64_t rows, int64_t st, int64_t sh, int32_t heads, int32_t d) 
 
 bool cache_fine(const la_paged_cache* c) {
   if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->block_table) return false;
-  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16)) return false;
+  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(c->block_table, 4))
+    return false;
   if (c->head_dim != 64 && c->head_dim != 128) return false;
   if (c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128) return false;
   return c->num_pages >= 1 && c->heads >= 1 && c->heads <= 65535 && c->batch >= 1 && c->batch <= 65535 && c->max_pages >= 1 &&
@@ -153,7 +155,9 @@ int la_op_cache_append_fp8(const la_paged_cache* cache, int32_t dtype, const voi
     return LA_EINVAL;
   RotaryTable tab;
   if (!fill_table(tab, cache->head_dim, naxes, pairs, theta, half, 0)) return LA_EINVAL;
-  if (!cu_new || !cache_len || (tab.n > 0 && tokens > 0 && !pos)) return LA_EINVAL;
+  if (!cu_new || !cache_len || (tab.n > 0 && tokens > 0 && !pos) || !aligned(cu_new, 4) || !aligned(cache_len, 4) ||
+      !aligned(pos, 4))
+    return LA_EINVAL;
   if (tokens == 0 || max_new == 0) return LA_OK;
   if (!k || !v || !aligned(k, elem_size(dtype)) || !aligned(v, elem_size(dtype))) return LA_EINVAL;
   CacheAppendParams p{};
@@ -206,7 +210,7 @@ int la_op_attention_cache_fp8(const la_paged_cache* cache, int32_t dtype, const 
       !strides_fit(tokens, out_token_stride, out_head_stride, heads, cache->head_dim) ||
       !rows_apart(tokens, out_token_stride, out_head_stride, heads, cache->head_dim))
     return LA_EINVAL;
-  if (!cu_q || !kv_len) return LA_EINVAL;
+  if (!cu_q || !kv_len || !aligned(cu_q, 4) || !aligned(kv_len, 4)) return LA_EINVAL;
   const int64_t need = la_op_attention_cache_fp8_workspace(cache, tokens, heads, max_q, max_kv);
   if (need < 0 || workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 16)))) return LA_EINVAL;
   if (tokens == 0 || max_q == 0) return LA_OK;

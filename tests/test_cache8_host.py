@@ -132,7 +132,8 @@ def _cache(**over):
 CACHE_BAD = [dict(k_pages=None), dict(v_pages=None), dict(k_scale=None), dict(v_scale=None), dict(block_table=None),
              dict(k_pages=BUF + 8), dict(v_pages=BUF + 4), dict(num_pages=0), dict(heads=0), dict(heads=65536),
              dict(page_tokens=16), dict(page_tokens=63), dict(page_tokens=256), dict(head_dim=96), dict(head_dim=256),
-             dict(batch=0), dict(batch=65536), dict(max_pages=0), dict(max_pages=1 << 26)]
+             dict(k_scale=BUF + 2), dict(v_scale=BUF + 1), dict(block_table=BUF + 2), dict(batch=0), dict(batch=65536),
+             dict(max_pages=0), dict(max_pages=1 << 26)]
 
 
 def _append(lib, cache=None, dtype=0, k=BUF, kt=128, kh=64, v=BUF, vt=128, vh=64, tokens=2, cu=BUF, lens=BUF, max_new=2,
@@ -146,7 +147,7 @@ def _append(lib, cache=None, dtype=0, k=BUF, kt=128, kh=64, v=BUF, vt=128, vh=64
 @pytest.mark.parametrize("over", CACHE_BAD + [
     dict(dtype=3), dict(k=None), dict(v=None), dict(cu=None), dict(lens=None), dict(pos=None), dict(tokens=-1),
     dict(max_new=-1), dict(kt=0), dict(kh=63), dict(vt=-1), dict(vh=1), dict(pairs=(33,)), dict(pairs=(0,)), dict(theta=0.0),
-    dict(k=BUF + 1), dict(dtype=1, v=BUF + 2),
+    dict(k=BUF + 1), dict(dtype=1, v=BUF + 2), dict(cu=BUF + 2), dict(lens=BUF + 1), dict(pos=BUF + 2),
 ])
 def test_append_refuses(lib, over):
     assert _append(lib, **over) == _lib.LA_EINVAL
@@ -171,7 +172,7 @@ def _attn(lib, dtype=0, q=BUF, qt=256, qh=64, tokens=2, q_heads=4, cu=BUF, lens=
     dict(q_heads=0), dict(max_q=-1), dict(max_kv=-1), dict(causal=-1), dict(scale=0.0), dict(scale=-1.0),
     dict(scale=float("nan")), dict(scale=float("inf")), dict(qh=63), dict(qt=-1), dict(ot=0), dict(ot=64, oh=64), dict(ot=128, oh=64), dict(oh=66), dict(ot=258),
     dict(out=BUF + 4), dict(q=BUF + 1), dict(out32=BUF + 8), dict(max_kv=1 << 20, ws_bytes=0), dict(max_kv=1 << 20, ws=None),
-    dict(max_kv=1 << 20, ws=BUF + 8),
+    dict(max_kv=1 << 20, ws=BUF + 8), dict(cu=BUF + 2), dict(lens=BUF + 2),
 ])
 def test_attention_refuses(lib, over):
     assert _attn(lib, **over) == _lib.LA_EINVAL
