@@ -394,9 +394,13 @@ def _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev):
                              num, heads, page, d, batch, width)
 
 
-def _like(x, out, name="out"):
+def _like(x, out, stream, name="out"):
+    """out checked, or a new tensor like x that the allocator keeps for the call's stream."""
     if out is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
+        if stream is None:
+            return torch.empty_like(x, memory_format=torch.contiguous_format)
+        with torch.cuda.stream(stream):
+            return torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError(f"{name}: expected {x.dtype} {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
     return out
@@ -410,7 +414,7 @@ def op_rope_axes(x, pos, pairs, out=None, theta=10000.0, half=False, inverse=Fal
     lib = load()
     px, xt, xh = _rows(x, "x")
     dev = x.get_device()
-    out = _like(x, out)
+    out = _like(x, out, stream)
     po, ot, oh = _rows(out, "out", dev)
     tokens, heads, d = x.shape
     pp, n, arr = _axes(pos, pairs, tokens, dev)
@@ -458,7 +462,7 @@ def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, k
     lib = load()
     pq, qt, qh = _rows(q, "q", None, _HALVES)
     dev = q.get_device()
-    out = _like(q, out)
+    out = _like(q, out, stream)
     po, ot, oh = _rows(out, "out", dev)
     c = _cache(k_pages, v_pages, k_scale, v_scale, block_table, dev)
     tokens, heads, d = q.shape

@@ -587,15 +587,19 @@ def test_on_another_stream_and_captured_twice():
 
 
 def test_stream_argument_and_device_checks():
-    from streaming_causal_video_timestep_b200 import op_rope_axes
+    from streaming_causal_video_timestep_b200 import op_attention_cache_fp8, op_rope_axes
     x, pos = rand(0, 4, 2, 64), i32(np.arange(12).reshape(4, 3))
     ref = op_rope_axes(x, pos, PAIRS[64])
+    c, q, kv, cu = filled(60, 1, [3000], 2, 64, 64), rand(61, 1, 2, 64), i32([3000]), i32([0, 1])
+    want = op_attention_cache_fp8(q, *c.g, kv, cu, 1, 3000)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     out = torch.empty_like(x)
     op_rope_axes(x, pos, PAIRS[64], out=out, stream=side)
+    made = op_rope_axes(x, pos, PAIRS[64], stream=side)
+    got = op_attention_cache_fp8(q, *c.g, kv, cu, 1, 3000, stream=side)
     side.synchronize()
-    assert torch.equal(out, ref)
+    assert torch.equal(out, ref) and torch.equal(made, ref) and torch.equal(got, want)
 
 
 def test_microbenchmarks_run(monkeypatch):
