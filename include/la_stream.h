@@ -408,9 +408,10 @@ int la_debug_wait_timeout(int64_t limit_ns, int32_t complete, int32_t* device_er
 int la_debug_op_wait_timeout(int64_t limit_ns, void* cuda_stream);
 
 /* ---- op-level entry points (unit tests, microbenchmarks) ------------------
- * Each enqueues one kernel on cuda_stream (a cudaStream_t, NULL = default).
- * They allocate nothing except where stated.  Their tensor-core kernels wait
- * on mbarriers with a limit, like the stream's; a wait that gives up raises a
+ * Each enqueues one kernel on cuda_stream (a cudaStream_t, NULL = default);
+ * la_op_attention_cache_fp8 a second one where it splits the keys.  They
+ * allocate nothing except where stated.  Their tensor-core kernels wait on
+ * mbarriers with a limit, like the stream's; a wait that gives up raises a
  * per-device op-level error word (a file-scope device int of the library,
  * first error wins) and the kernel returns with its output unfinished.
  */
@@ -650,10 +651,10 @@ int la_op_cache_append_fp8(const la_paged_cache* cache, int32_t dtype, const voi
  * it NaN.
  * max_kv, a bound of kv_len, steers the split of the keys only.  workspace:
  * DEVICE, 16-byte aligned, at least la_op_attention_cache_fp8_workspace bytes for
- * the same arguments (0: may be NULL); calls that may run at the same time need
- * one each.  Results do not depend on what it holds.  A sequence or page that
- * does not fit the arrays is reported as by the append (its rows are not
- * written; keys of a bad page are not seen).
+ * the same arguments (0: may be NULL; negative: LA_EINVAL); calls that may run
+ * at the same time need one each.  Results do not depend on what it holds.  A
+ * sequence or page that does not fit the arrays is reported as by the append (its
+ * rows are not written; keys of a bad page are not seen).
  */
 int64_t la_op_attention_cache_fp8_workspace(const la_paged_cache* cache, int64_t tokens,
                                             int32_t heads, int64_t max_q, int64_t max_kv);

@@ -62,7 +62,7 @@ template <int D> constexpr size_t rows_smem() {
 
 // HALVES: 8-row halves of the MMA's 16 rows that hold rows of this call; an empty half
 // costs its part of the softmax otherwise (at 1 row, 16 x 40 heads over up to 14040 keys:
-// 258 us, 270 with both).
+// 261 us, 270 with both).
 template <typename T, int D, int HALVES>
 __global__ void __launch_bounds__(WARPS * 32, 3)
 k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {

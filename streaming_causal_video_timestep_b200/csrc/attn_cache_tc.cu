@@ -464,8 +464,8 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
           }
         }
         // At D = 64 the first half of P is handed over as soon as it is there: its products
-        // run beside the second half's exponentials (4 prompts of up to 1013 rows: 108 us,
-        // 114 in one).  At D = 128 that was slower (1717 us at 4680 x 15600 x 40, 1567).
+        // run beside the second half's exponentials (4 prompts of up to 1013 rows: 112.8
+        // us, 113.4 in one).  At D = 128 that was slower (1720 us at 4680 x 15600 x 40, 1575).
         l *= alpha;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

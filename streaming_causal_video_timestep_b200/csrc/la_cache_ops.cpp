@@ -75,14 +75,14 @@ bool cache_fine(const la_paged_cache* c) {
 bool few_rows(int64_t max_q, int32_t heads, int32_t kv_heads) { return max_q * (heads / kv_heads) <= LA_CACHE_FEW_ROWS; }
 
 // How a call is laid out.  Few rows: enough CTAs for 3 on every SM with at least 128
-// keys each (one token over 1561 keys x 8 heads: 9.7 us; 10.9 with 256), and pieces of
+// keys each (one token over 1561 keys x 8 heads: 10.0 us; 11.0 with 256), and pieces of
 // about 2048 keys where that makes more, which evens out ragged lengths (16 x 40 heads
-// over up to 14040 keys: 258 us; 343 unsplit, 285 with 1024 keys).
+// over up to 14040 keys: 261 us; 309 unsplit, 278 with 1024 keys).
 // Many rows: one CTA an SM, 256 rows of a (sequence, key head) each.  The units behind
 // the last full round of the SMs are split along the keys, into the number of pieces that
 // makes the fewest key tiles in a row, a piece counted two tiles longer than it is for
-// its start and end and its part of the join (760 units of 122 tiles: 1698 us
-// unsplit, 1685 with the last 20 in 7 pieces each).
+// its start and end and its part of the join (760 units of 122 tiles: 1735 us
+// unsplit, 1575 with the last 20 in 7 pieces each).
 struct Plan {
   int nsplit = 1, pairs = 0, full = 0, units = 0;
   int64_t part_rows = 0;                           // of all pieces
