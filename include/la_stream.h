@@ -592,7 +592,8 @@ int la_op_rope_axes(int32_t dtype, const void* x, int64_t x_token_stride, int64_
 typedef struct la_paged_cache {
   void* k_pages;               /* uint8 [num_pages, heads, page_tokens, head_dim], 16-byte aligned */
   void* v_pages;
-  float* k_scale;              /* fp32 [num_pages, heads], positive (NaN: see the append) */
+  float* k_scale;              /* fp32 [num_pages, heads], 2^-64 to 2^120 as the append
+                                  leaves them (NaN: see there) */
   float* v_scale;
   const int32_t* block_table;  /* int32 [batch, max_pages] */
   int32_t num_pages;

@@ -23,7 +23,9 @@
 //     spreads the rows that one quarter warp reads over the swizzle in both products.
 // e4m3 codes are exact in fp16; q is scaled to fp16 by a power of two per row.  The
 // key page's scale multiplies the scores; the value page's scale enters P's exponent
-// (and leaves the normaliser again), so P V needs no multiplications of its own.
+// (and leaves the normaliser again), so P V needs no multiplications of its own.  Where
+// scales lie so far apart that P flushes to 0, the normaliser does without them (see
+// LA_CACHE_SPREAD).
 #include "attn_cache.cuh"
 
 namespace {
@@ -178,7 +180,7 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
       }
   }
   float o[D / 8][4];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, top_lv = -INFINITY;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -207,7 +209,10 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
       }
     }
     // x[nt][2 i + e]: row n + 8 i, key 8 nt + ((2 c + e) ^ 4 e)
-    const float lv = __log2f(vs), rv = __frcp_rn(vs);
+    const float lv = __log2f(vs);
+    float rv = __frcp_rn(vs);
+    const bool far = lv < top_lv - LA_CACHE_SPREAD;          // of all the steps before
+    top_lv = fmaxf(top_lv, lv);
     float mt[HALVES];
     const bool full = st * 16 + 16 <= low;                   // no row of the tile is masked here
 #pragma unroll
@@ -228,22 +233,30 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     }
     bool need = mt[0] > m[0] + LA_CACHE_P_TAU;
     if (HALVES == 2) need = need || mt[HALVES - 1] > m[HALVES - 1] + LA_CACHE_P_TAU;
-    if (__any_sync(0xffffffffu, need)) {
+    if (__any_sync(0xffffffffu, need || far)) {
 #pragma unroll
       for (int i = 0; i < HALVES; ++i) {
         float t = mt[i];
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
         const float mn = fmaxf(m[i], t);
-        const float al = m[i] == mn ? 1.0f : fast_exp2(m[i] - mn);    // -inf first: 0
+        const float h = m[i] == mn ? 1.0f : fast_exp2(0.5f * (m[i] - mn)), al = h * h;    // -inf first: 0
         m[i] = mn;
-        l[i] *= al;
+        l[i] = l[i] * h * h;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
           o[j][2 * i] *= al;
           o[j][2 * i + 1] *= al;
         }
+        if (far) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float t = x[k >> 1][2 * i + (k & 1)], h = fast_exp2(0.5f * (t - lv + (LA_CACHE_P_BIAS - mn)));
+            if (t != -INFINITY) l[i] += h * h;
+          }
+        }
       }
+      if (far) rv = 0.f;                         // counted
     }
     uint32_t pa[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -307,8 +320,8 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
     float L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      const float f = sm[w][r] == M ? 1.0f : fast_exp2(sm[w][r] - M);
-      L += sl[w][r] * f;
+      const float h = sm[w][r] == M ? 1.0f : fast_exp2(0.5f * (sm[w][r] - M)), f = h * h;
+      L += sl[w][r] * h * h;
 #pragma unroll
       for (int e = 0; e < 4; ++e) a[e] += so[w][r][d4 + e] * f;
     }
@@ -368,8 +381,8 @@ k_attn_cache_join(const __grid_constant__ AttnCacheParams p, int wpr) {
       const int mine = i0 + lane * wpr;
       float2 w = make_float2(-INFINITY, 0.f);
       if (mine < p.nsplit) w = ml[mine * all];
-      const float f = w.x == M ? 1.0f : fast_exp2(w.x - M);
-      if (mine < p.nsplit) L += w.y * f;
+      const float h = w.x == M ? 1.0f : fast_exp2(0.5f * (w.x - M)), f = h * h;
+      if (mine < p.nsplit) L += w.y * h * h;
       const int n = min(32, (p.nsplit - i0 + wpr - 1) / wpr);
 #pragma unroll 8
       for (int k = 0; k < n; ++k) {
@@ -398,9 +411,9 @@ k_attn_cache_join(const __grid_constant__ AttnCacheParams p, int wpr) {
     L = 0.f;
     a[0] = a[1] = a[2] = a[3] = 0.f;
     for (int w = 0; w < wpr; ++w) {
-      const float f = sm[warp + w] == X ? 1.0f : fast_exp2(sm[warp + w] - X);
+      const float h = sm[warp + w] == X ? 1.0f : fast_exp2(0.5f * (sm[warp + w] - X)), f = h * h;
       const float4 v = so[warp + w][lane];
-      L += sl[warp + w] * f;
+      L += sl[warp + w] * h * h;
       a[0] += v.x * f; a[1] += v.y * f; a[2] += v.z * f; a[3] += v.w * f;
     }
   }

@@ -13,6 +13,16 @@
 // cost 2 % at 4680 x 15600 x 40 x 128.
 #define LA_CACHE_P_BIAS 7.0f
 #define LA_CACHE_P_TAU 8.0f
+// The normaliser counts 2^(s - M + P_BIAS) of every key, s its score alone: a sum of P
+// over the page's value scale.  Value scales reach from 2^-64 to 2^120 (the append's),
+// so the keys that matter make that a normal fp32 number (M is within P_TAU of a largest
+// t, hence at most 2^120 above the largest score), but P on the way to it, or a factor
+// between two maxima, may lie below 2^-126 and flush to 0.  Hence:
+//   * keys of a page whose value scale lies more than 2^SPREAD below the largest before
+//     it are summed without the scale; of the others, 2^-126 / vs at most is flushed,
+//     2^(SPREAD - 133) of the normaliser;
+//   * sums are taken from one maximum to another by 2^((M - M') / 2), twice.
+#define LA_CACHE_SPREAD 90.0f
 
 // Programmatic launch: the next grid of the stream may start, and waits here for the
 // end of the grid before it.

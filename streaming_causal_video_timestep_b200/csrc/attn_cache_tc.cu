@@ -22,7 +22,10 @@
 // Scales: the score of a key is acc * ks * (row factor); log2(vs) enters the
 // exponent, so a page's P carries its value scale and the normaliser takes it out
 // again (sum * 1 / vs): scales cost no instruction an element beyond the scale and
-// offset that the exponent needs anyway.
+// offset that the exponent needs anyway.  A tile with a page whose value scale lies far
+// below an earlier one (see LA_CACHE_SPREAD) gets 0 for 1 / vs, and its weights are
+// summed by themselves, without the scales; the others pay 0 to 1.5 % for the question
+// (2 x 4680 q x 7800 keys x 16 heads, frame-causal: 594 us a call, 587 without).
 #include <cstdio>
 
 #include "attn_cache.cuh"
@@ -78,12 +81,13 @@ __device__ __forceinline__ void ld_wait(uint32_t (&u)[32]) {
 }
 
 // The running maximum of a row over a key tile's scores (raw accumulators in tensor
-// memory, log2 domain with the value scale) and what it makes of the old one.  sc[c]: a
-// 32-key chunk's (ks, log2 vs, 1 / vs).  The scores are read twice, 32 at a time, once
-// here: 128 of them held at once would not fit beside the other warps' registers.
+// memory, log2 domain with the value scale); root: the square root of the factor that
+// takes sums from the old one to it.  sc[c]: a 32-key chunk's (ks, log2 vs, 1 / vs).
+// The scores are read twice, 32 at a time, once here: 128 of them held at once would not
+// fit beside the other warps' registers.
 template <bool MASKED>
 __device__ __forceinline__ void softmax_max(uint32_t s_base, int valid, float rowf, const float4* sc, float& m_ref,
-                                            float& alpha) {
+                                            float& root) {
   uint32_t u[2][32];
   float mt = -INFINITY;
   tmem_ld32(s_base, u[0]);
@@ -108,8 +112,29 @@ __device__ __forceinline__ void softmax_max(uint32_t s_base, int valid, float ro
   }
   const bool need = mt > m_ref + LA_CACHE_P_TAU;
   const float mn = need ? mt : m_ref;
-  alpha = need ? fast_exp2(m_ref - mn) : 1.0f;
+  root = need ? fast_exp2(0.5f * (m_ref - mn)) : 1.0f;
   m_ref = mn;
+}
+
+// The row's share of a tile in the normaliser, straight from the scores.
+__device__ __forceinline__ float softmax_sum(uint32_t s_base, int valid, float rowf, const float4* sc, float m_ref) {
+  const float base = LA_CACHE_P_BIAS - (m_ref == -INFINITY ? 0.f : m_ref);
+  float l = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t u[32];
+    tmem_ld32(s_base + c * 32, u);
+    ld_wait(u);
+    const float4 v = sc[c];
+    const float a = v.x * rowf;
+    const int n = v.w == 0.f ? 0 : valid - 32 * c;             // keys of no page are not seen
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float h = fast_exp2(0.5f * fmaf(__uint_as_float(u[i]), a, base));
+      if (i < n) l += h * h;
+    }
+  }
+  return l;
 }
 
 // The row's P (fp16 pairs) of 64 keys, chunks c0 and c0 + 1, stored over scores that both
@@ -240,6 +265,7 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       const int span = min(128, p.page_tokens);
       int t = 0;
       bool ok = true;
+      float top_lv = -INFINITY;
       for (; t < nt && ok; ++t) {
         const int key = (t0 + t) * 128 + 32 * lane;
         int pg = -1;
@@ -255,6 +281,16 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
             if ((32 * lane) % span == 0) bytes = static_cast<uint32_t>(min(span, keys - key)) * D;
           }
         }
+        float low = pg >= 0 ? v.y : INFINITY;
+        top_lv = fmaxf(top_lv, pg >= 0 ? v.y : -INFINITY);
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+          top_lv = fmaxf(top_lv, __shfl_xor_sync(0xffffffffu, top_lv, o));
+        }
+        // a tile whose first page is not there is summed in that way, too
+        const int first = __shfl_sync(0xffffffffu, pg, 0);
+        if (first < 0 || low < top_lv - LA_CACHE_SPREAD) v.z = 0.f;
         uint32_t all = bytes;
         all += __shfl_xor_sync(0xffffffffu, all, 1);
         all += __shfl_xor_sync(0xffffffffu, all, 2);
@@ -446,15 +482,20 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
           break;
         }
         tc_fence_after();
-        float alpha;
+        float root;
         const float4* sc = sS + (t % NSC) * 4;
         const bool full = __all_sync(0xffffffffu, valid >= 128);
-        if (full) softmax_max<false>(s_base, valid, rowf, sc, m_ref, alpha);
-        else softmax_max<true>(s_base, valid, rowf, sc, m_ref, alpha);
-        if (t >= 1 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-          // O is stable: the commit that signalled S(t) also covers PV(t-1), issued before it
+        if (full) softmax_max<false>(s_base, valid, rowf, sc, m_ref, root);
+        else softmax_max<true>(s_base, valid, rowf, sc, m_ref, root);
+        const bool apart = sc->z == 0.f;          // the same in every lane
+        if (__any_sync(0xffffffffu, root != 1.0f || apart)) {
+          const float alpha = root * root;
+          l = l * root * root;
+          if (apart) l += softmax_sum(s_base, valid, rowf, sc, m_ref);
+          // O is stable: the commit that signalled S(t) also covers PV(t-1), issued before
+          // it; the first tile finds nothing in it
 #pragma unroll 1
-          for (int c4 = 0; c4 < D / 32; ++c4) {
+          for (int c4 = t >= 1 ? 0 : D / 32; c4 < D / 32; ++c4) {
             uint32_t o[32];
             tmem_ld32(o_base + c4 * 32, o);
             ld_wait(o);
@@ -466,7 +507,6 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
         // At D = 64 the first half of P is handed over as soon as it is there: its products
         // run beside the second half's exponentials (4 prompts of up to 1013 rows: 112.8
         // us, 113.4 in one).  At D = 128 that was slower (1720 us at 4680 x 15600 x 40, 1575).
-        l *= alpha;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           l += full ? softmax_exp<false>(s_base, 2 * h, valid, rowf, sc, m_ref)

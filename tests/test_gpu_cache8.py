@@ -433,6 +433,50 @@ def test_attention_peaked_and_far_apart(nq, G):
     check_attention(c, q.bfloat16(), [L], [0, nq], 0, scale=1e-3)
 
 
+@pytest.mark.parametrize("tilt", [False, True])
+@pytest.mark.parametrize("max_kv", [0, 5000])
+@pytest.mark.parametrize("page,d", [(64, 128), (32, 64), (128, 128), (32, 128)])
+@pytest.mark.parametrize("nq,G", [(1, 1), (3, 4), (150, 2)])
+def test_attention_value_scales_far_apart(nq, G, page, d, max_kv, tilt):
+    """Pages of zeros (scale 2^-64) beside values up to 1e37 (2^116), in every order, whole and in pieces; tilt: the
+    large values lie where the weights are smallest.  Every key counts in the normaliser.
+
+    The bound is the module's, with two changes.  An argument of an exponential is a score and log2 of a scale, of
+    magnitude S + 128 at most, rounded three times (with the scale, the maximum, and where the scale is taken out
+    again): 3 * 128 u ln 2 < 300 u more a P.  And P, stored with 2^-24 for its last place under a maximum M of
+    score + log2 scale, is off by 2^-25 2^(M - 7) at most; M is no larger than the largest p_j vs_j, so
+    L * 2^-32 * 448 * max_j p_j vs_j."""
+    L = 11 * page - 7
+    grade = np.array([0.0, 1e24, 1.0, 0.0, 1e37, 1e-18, 1e24, 0.0, 1.0, 1e37, 0.0])[:, None]    # of each page's values
+    nats = np.array([0.0, -10, 0, 3, -20, 30, -11, 1, -1, -21, 0])                              # and of its scores
+    for turn in (0, 4, 7):
+        c = Cache(28, 1, 12, 1, page, d)
+        g, t = np.roll(grade, turn).repeat(page)[:L], np.roll(nats, turn).repeat(page)[:L]
+        k, v = rand(1, L, 1, d, dtype="fp32"), rand(2, L, 1, d, dtype="fp32")
+        v *= torch.from_numpy(g.astype(np.float32)).cuda()[:, None, None]
+        q = rand(3, nq, G, d, dtype="fp32")
+        if tilt:
+            k[:, 0, 0] = torch.from_numpy(t.astype(np.float32)).cuda()
+            q[..., 0] = d ** 0.5
+        else:
+            q[0] = 0                                                           # equal scores: an average over all keys
+        c.append(k, v, [0], [0, L])
+        q = q.bfloat16()
+        out, o32 = attend(c, q, [L], [0, nq], 0, max_kv=max_kv)
+        pages, scales = [x.cpu().numpy() for x in c.g[:2]], [x.cpu().numpy() for x in c.g[2:4]]
+        kk, vv = (dense_cache(pages[i], scales[i], c.table, 0, L)[:, 0] for i in range(2))
+        vs = scales[1].astype(np.float64)[c.table[0, np.arange(L) // page], 0]
+        x = np.einsum("nhd,ld->nhl", np64(q), kk) * d ** -0.5
+        s = (np.einsum("nhd,ld->nhl", np.abs(np64(q)), np.abs(kk)) * d ** -0.5).max(-1, keepdims=True)
+        p = np.exp(x - x.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        p_err = 2 * ((d + 8) * U * s + 4 * U) + 300 * U
+        bound = (p @ np.abs(vv)) * (2.0 ** -11 + 2 * p_err + 2 * (L / 16 + 64) * 2 * U)
+        bound = bound + L * 2.0 ** -32 * 448 * (p * vs).max(-1, keepdims=True)
+        near(np64(o32), p @ vv, bound, f"out32, turn {turn}")
+        near(np64(out), p @ vv, bound * 1.01 + half_step(p @ vv, q.dtype) * 1.01, f"out, turn {turn}")
+
+
 @pytest.mark.parametrize("nq", [1, 70])
 def test_attention_does_not_see_what_is_masked(nq):
     """NaN scales of pages behind the length, NaN codes behind the last key, and a marked page that no row sees."""
