@@ -19,6 +19,10 @@
 // tile waits for the loads that are under way for the next one (1.96 ms against
 // 1.57 ms at 4680 x 15600 x 40 x 128).
 //
+// Waits are bounded.  Lanes of a warp may see one end differently (each looks at the
+// clock and at the CTA's abort flag by itself), and what follows needs all of them, so
+// every answer is put to a vote.
+//
 // Scales: the score of a key is acc * ks * (row factor); log2(vs) enters the
 // exponent, so a page's P carries its value scale and the normaliser takes it out
 // again (sum * 1 / vs): scales cost no instruction an element beyond the scale and
@@ -299,7 +303,7 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
         // the codes of tile t - 1 were unpacked into a K stage that the scores of tile
         // t - 1 - NS freed, which were issued behind the P of tile t - 2 - NS >= t - NSC.
         for (int i = 0; i < 2 && ok; ++i) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&raw_empty[i], (t & 1) ^ 1, err)) && !abort_flag;
+          ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait(&raw_empty[i], (t & 1) ^ 1, err));
           if (!ok) break;
           if (i == 0 && lane < 4) sS[(t % NSC) * 4 + lane] = v;
           __syncwarp();
@@ -401,13 +405,13 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
             make_uint4(e4m3x2_f16x2_lo(w.z), e4m3x2_f16x2_hi(w.z), e4m3x2_f16x2_lo(w.w), e4m3x2_f16x2_hi(w.w));
       }
     };
-    for (int t = 0; t < nt && !abort_flag; ++t) {
+    for (int t = 0; t < nt; ++t) {
       const uint32_t st = t % NS, par = (t / NS) & 1;
       bool ok = true;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        ok = ok && mbar_wait(&raw_full[i], t & 1, err) && mbar_wait(i ? &v_empty[st] : &k_empty[st], par ^ 1, err);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait(&raw_full[i], t & 1, err) &&
+                                         mbar_wait(i ? &v_empty[st] : &k_empty[st], par ^ 1, err));
         if (!ok) break;
         unpack(raw + i * 128 * D, (i ? sV : sK) + st * TILE, t);
         fence_proxy_async_smem();
@@ -476,11 +480,9 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       bool ok = true;
       for (int t = 0; t < nt; ++t) {
         const int valid = lim - (t0 + t) * 128;
-        if (abort_flag || !mbar_wait(&sc_full[t % NSC], static_cast<uint32_t>((t / NSC) & 1), err) ||
-            !mbar_wait(&s_full[w], static_cast<uint32_t>(t & 1), err)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait(&sc_full[t % NSC], static_cast<uint32_t>((t / NSC) & 1), err) &&
+                                         mbar_wait(&s_full[w], static_cast<uint32_t>(t & 1), err));
+        if (!ok) break;
         tc_fence_after();
         float root;
         const float4* sc = sS + (t % NSC) * 4;
@@ -520,7 +522,8 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       }
       if (!ok) abort_flag = 1;
       const long long part = (static_cast<long long>(split) * (p.units - p.full) + unit - p.full) * 256 + w * 128 + r;
-      if (ok && (nt == 0 || mbar_wait(&pv_done[w], 0, err))) {
+      ok = __all_sync(0xffffffffu, ok && (nt == 0 || mbar_wait(&pv_done[w], 0, err)));
+      if (ok) {
         tc_fence_after();
         if (!whole && on) p.part_ml[part] = make_float2(m_ref, l);
 #pragma unroll 1

@@ -199,3 +199,32 @@ def test_binding_refuses_what_is_not_on_a_gpu():
         op_cache_append_fp8(x, x, None, None, None, None, None, None, None, 1)
     with pytest.raises(TypeError):
         op_attention_cache_fp8(x, None, None, None, None, None, None, None, 1, 1)
+
+
+def test_waits_of_the_attention_kernel_are_decided_by_the_warp():
+    """A bounded wait may end differently from lane to lane (each looks at the clock, and at the CTA's abort flag, by
+    itself), and what follows it needs the whole warp: every answer, and every look at the flag, goes through a vote."""
+    import os
+    import re
+    src = os.path.join(os.path.dirname(_lib.__file__), "csrc", "attn_cache_tc.cu")
+    text = re.sub(r"//[^\n]*", "", open(src).read())
+    seen = 0
+    for s in re.split(r"[;{}]", text):
+        s = " ".join(s.split())
+        reads = re.search(r"\babort_flag\b(?! = )", s) and "volatile" not in s
+        if "mbar_wait(" not in s and not reads:
+            continue
+        seen += 1
+        alone = re.match(r"(for \([^)]*\) )?(if \(!ok && t > 1\) )?mbar_wait\(", s)    # nothing depends on its answer
+        assert alone or re.search(r"__all_sync\(0xffffffffu, [^;]*(mbar_wait|abort_flag)", s), s
+        if not alone:
+            vote = s.index("__all_sync(")
+            assert all(m.start() > vote for m in re.finditer(r"mbar_wait\(|\babort_flag\b", s)), s
+            depth, end = 0, vote + len("__all_sync")
+            while True:                                            # the vote's own parentheses hold all of them
+                depth += {"(": 1, ")": -1}.get(s[end], 0)
+                end += 1
+                if depth == 0:
+                    break
+            assert not re.search(r"mbar_wait\(|\babort_flag\b", s[end:]), s
+    assert seen >= 7
