@@ -447,10 +447,10 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
       if (on && !p.q_vec) {
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          T e[8];
+          uint32_t e[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) e[k] = q[8 * c + k];
-          raw_q[c] = *reinterpret_cast<uint4*>(e);
+          for (int k = 0; k < 8; ++k) e[k] = reinterpret_cast<const unsigned short*>(q)[8 * c + k];
+          raw_q[c] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
         }
       }
 #pragma unroll

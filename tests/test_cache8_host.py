@@ -228,3 +228,19 @@ def test_waits_of_the_attention_kernel_are_decided_by_the_warp():
                     break
             assert not re.search(r"mbar_wait\(|\babort_flag\b", s[end:]), s
     assert seen >= 7
+
+
+def test_local_arrays_read_as_vectors_are_aligned():
+    """A local array that is read or written as 8- or 16-byte vectors has to be declared with that alignment: its
+    element type alone does not give it."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(_lib.__file__), "csrc")
+    bad = []
+    for name in sorted(os.listdir(csrc)):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        for m in re.finditer(r"^[ \t]*((?:T|TO|__half|__nv_bfloat16|u?int(?:8|16|32)_t|float|unsigned(?: char| short)?) (\w+)(?:\[\w+\])+);", text, re.M):
+            use = re.search(r"reinterpret_cast<(?:const )?(?:uint2|uint4|float4|longlong2)\*>\(&?" + m[2] + r"\b", text[m.end():].split("\n}", 1)[0])   # to the function's end
+            if use:
+                bad.append(f"{name}: {m[1]}")
+    assert not bad, bad
