@@ -406,13 +406,39 @@ def _like(x, out, stream, name="out"):
     return out
 
 
+class _RopeAxes(torch.autograd.Function):
+    """op_rope_axes with its gradient: the rotation turned back."""
+
+    @staticmethod
+    def forward(ctx, x, pos, pairs, theta, half, inverse):
+        out = op_rope_axes(x, pos, pairs, None, theta, half, inverse)
+        ctx.save_for_backward(pos)
+        ctx.call = tuple(pairs), theta, half, inverse
+        return out
+
+    @staticmethod
+    def backward(ctx, g):
+        (pos,), (pairs, theta, half, inverse) = ctx.saved_tensors, ctx.call
+        if g.stride(2) != 1 or 0 in g.stride():     # expanded, or head_dim not innermost
+            g = g.contiguous()
+        return op_rope_axes(g, pos, pairs, None, theta, half, not inverse), None, None, None, None, None
+
+
 def op_rope_axes(x, pos, pairs, out=None, theta=10000.0, half=False, inverse=False, stream=None):
     """Rotary positions with several axes (la_op_rope_axes): x [tokens, heads, head_dim] bf16, fp16 or fp32
     (any token and head strides), pos int32 [tokens, axes], pairs: rotary pairs of each axis.  half: pair i is
     elements (i, i + n) instead of (2i, 2i+1).  inverse undoes the rotation: the gradient of x from that of
-    out.  out: a tensor like x (x itself: in place), made if None; returns out."""
+    out.  out: a tensor like x (x itself: in place), made if None; returns out.  Where x requires a gradient, the
+    returned tensor has one (through the same kernel), and out has to be None."""
     lib = load()
     px, xt, xh = _rows(x, "x")
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out: x requires a gradient, which is not recorded through a given output")
+        if stream is None:
+            return _RopeAxes.apply(x, pos, pairs, theta, half, inverse)
+        with torch.cuda.stream(stream):         # the backward pass runs where the call did
+            return _RopeAxes.apply(x, pos, pairs, theta, half, inverse)
     dev = x.get_device()
     out = _like(x, out, stream)
     po, ot, oh = _rows(out, "out", dev)
@@ -458,7 +484,7 @@ def op_attention_cache_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, k
     key visible; c: a sequence's queries are its last tokens, in blocks of c that see themselves and all before.
     scale: of the scores, 1/sqrt(head_dim) if None.  out: a tensor like q, made if None (zeros for rows that
     see no key; rows of no sequence are not written); out32: optional fp32 [tokens, heads, head_dim].
-    Returns out."""
+    Records no gradient (it reads a cache of codes).  Returns out."""
     lib = load()
     pq, qt, qh = _rows(q, "q", None, _HALVES)
     dev = q.get_device()

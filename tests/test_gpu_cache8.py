@@ -173,6 +173,84 @@ def test_rope_axes_of_no_tokens_and_refusals():
             op_rope_axes(**{"x": x, "pos": pos, "pairs": PAIRS[64], **bad})
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("half,inverse", [(False, False), (True, False), (False, True)])
+def test_rope_axes_gradient(half, inverse, dtype):
+    """The gradient is the rotation turned back: within the rotation's bound and one rounding of the definition; a
+    gradient that arrives expanded, transposed or strided gives the same."""
+    from streaming_causal_video_timestep_b200 import op_rope_axes
+    T, H, d, pairs = 13, 3, 128, (20, 21, 6)
+    pos = np.random.default_rng(5).integers(-300, 9000, (T, 3))
+    x = rand(11, T, H, d, dtype=dtype).requires_grad_()
+    y = op_rope_axes(x, i32(pos), pairs, half=half, inverse=inverse)
+    assert y.requires_grad and torch.equal(y.detach(), op_rope_axes(x.detach(), i32(pos), pairs, half=half, inverse=inverse))
+    wide = rand(12, T, H, d + 4, dtype=dtype)
+    for g in (rand(13, T, H, d, dtype=dtype), wide[..., 1:d + 1], rand(14, H, T, d, dtype=dtype).transpose(0, 1),
+              rand(15, T, d, H, dtype=dtype).transpose(1, 2), rand(16, 1, 1, d, dtype=dtype).expand(T, H, d),
+              torch.ones((), dtype=DT[dtype], device="cuda").expand(T, H, d)):
+        (dx,) = torch.autograd.grad(y, x, g, retain_graph=True)
+        ref = rotate_axes(np64(g), pos, pairs, half=half, inverse=not inverse)
+        near(np64(dx), ref, turn_bound(np64(g), pairs, half) + half_step(ref, x.dtype) * (1 + 1e-5))
+        assert dx.dtype == x.dtype
+    y.backward(g)
+    y2 = op_rope_axes(x, i32(pos), pairs, half=half, inverse=inverse)
+    y2.backward(g)                                       # accumulates: twice the same
+    assert torch.equal(x.grad, (dx.float() * 2).to(x.dtype))
+
+
+def test_rope_axes_gradient_against_differences():
+    from streaming_causal_video_timestep_b200 import op_rope_axes
+    T, H, d = 4, 2, 64
+    pos, pairs = i32(np.random.default_rng(6).integers(0, 4000, (T, 2))), (9, 14)
+    x, w = rand(17, T, H, d, dtype="fp32").requires_grad_(), rand(18, T, H, d, dtype="fp32")
+    f = lambda v: float((op_rope_axes(v, pos, pairs).double() * w.double()).sum())  # noqa: E731
+    (dx,) = torch.autograd.grad(op_rope_axes(x, pos, pairs), x, w)
+    for i in ((0, 0, 0), (1, 1, 1), (2, 0, 17), (3, 1, 45), (3, 0, 46), (1, 0, 63)):
+        e = torch.zeros_like(x)
+        e[i] = 1.0
+        with torch.no_grad():
+            got = (f(x + e) - f(x - e)) / 2              # linear in x: only the two outputs that it moves are rounded
+        # x +- e rounds once (|x| < 8: 4 u), the output's bound is TURN (|x0| + |x1|) + u |y| at both of the pair, at both ends
+        bound = 2 * (2 * 16 * TURN + 16 * U + 8 * U) * float(w.abs().max())
+        assert abs(got - float(dx[i])) <= bound + TURN * 16
+    # twice: the gradient of the gradient is the rotation itself
+    g = rand(19, T, H, d, dtype="fp32").requires_grad_()
+    (dx,) = torch.autograd.grad(op_rope_axes(x, pos, pairs), x, g, create_graph=True)
+    (dg,) = torch.autograd.grad(dx, g, w)
+    assert torch.equal(dg, op_rope_axes(w, pos, pairs))
+
+
+def test_rope_axes_gradient_streams_graphs_and_refusals():
+    from streaming_causal_video_timestep_b200 import op_rope_axes
+    pos = i32(np.arange(300).reshape(100, 3))
+    x, g = rand(20, 100, 4, 128).requires_grad_(), rand(21, 100, 4, 128)
+    (want,) = torch.autograd.grad(op_rope_axes(x, pos, PAIRS[128]), x, g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = op_rope_axes(x, pos, PAIRS[128], stream=side)    # runs on side, and so does its backward
+    torch.cuda.current_stream().wait_stream(side)
+    (got,) = torch.autograd.grad(y, x, g)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (out,) = torch.autograd.grad(op_rope_axes(x, pos, PAIRS[128]), x, g)
+    g.copy_(rand(22, 100, 4, 128))
+    graph.replay()
+    (want,) = torch.autograd.grad(op_rope_axes(x, pos, PAIRS[128]), x, g)
+    assert torch.equal(out, want)
+    for out in (torch.empty_like(x), x):
+        with pytest.raises(ValueError, match="gradient"):
+            op_rope_axes(x, pos, PAIRS[128], out=out)
+    with torch.no_grad():
+        y = op_rope_axes(x, pos, PAIRS[128], out=torch.empty_like(x))
+    assert not y.requires_grad and not op_rope_axes(x.detach(), pos, PAIRS[128]).requires_grad
+    y = op_rope_axes(x, pos, PAIRS[128])
+    pos += 1                                             # positions that changed since: refused, not a wrong gradient
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, x, g)
+
+
 # ---- the cache ---------------------------------------------------------------------------------
 class Cache:
     """A paged cache on the GPU and the oracle's copy of it."""
