@@ -57,7 +57,8 @@ bool strides_fit(int64_t rows, int64_t st, int64_t sh, int32_t heads, int32_t d)
 }
 
 // An output's rows do not lie over one another: one of the two strides steps over all of the other's.
-bool rows_apart(int64_t rows, int64_t st, int64_t sh, int32_t heads, int32_t d) {
+// (128 bits: a stride may be 2^40, and 2^30 rows or 2^31 heads may lie that far apart.)
+bool rows_apart(__int128 rows, __int128 st, __int128 sh, int32_t heads, int32_t d) {
   return rows <= 1 || st >= (heads - 1) * sh + d || (heads == 1 ? st >= d : st >= d && sh >= (rows - 1) * st + d);
 }
 

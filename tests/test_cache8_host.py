@@ -244,3 +244,10 @@ def test_local_arrays_read_as_vectors_are_aligned():
             if use:
                 bad.append(f"{name}: {m[1]}")
     assert not bad, bad
+
+
+def test_outputs_whose_rows_overlap_are_refused_at_any_stride(lib):
+    """Strides whose products pass 64 bits: rows 2^40 apart, as are the heads, lie over one another."""
+    far = 1 << 40
+    assert _rope(lib, tokens=1 << 30, heads=3, xt=far, xh=far, ot=far, oh=far) == _lib.LA_EINVAL
+    assert _attn(lib, tokens=1 << 30, q_heads=(1 << 26) + 2, qt=far, qh=far, ot=far, oh=far, ws_bytes=1 << 62) == _lib.LA_EINVAL
