@@ -355,14 +355,16 @@ def _dense(t, dtype, shape, name, dev):
     raise TypeError(f"{name} must be a CUDA tensor")
 
 
+def _on(stream, dev):
+    """Checks that a given stream is of device `dev` (an index)."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+
+
 def _call(fn, dev, stream, *args):
     """fn(*args, stream handle) with `dev` the current device, on `stream` or the device's current one."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device.index != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
-    else:
-        handle = stream.cuda_stream
+    _on(stream, dev)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
         code = fn(*args, handle)
     else:
@@ -399,6 +401,7 @@ def _like(x, out, stream, name="out"):
     if out is None:
         if stream is None:
             return torch.empty_like(x, memory_format=torch.contiguous_format)
+        _on(stream, x.get_device())
         with torch.cuda.stream(stream):
             return torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.shape != x.shape or out.dtype != x.dtype:
@@ -437,6 +440,7 @@ def op_rope_axes(x, pos, pairs, out=None, theta=10000.0, half=False, inverse=Fal
             raise ValueError("out: x requires a gradient, which is not recorded through a given output")
         if stream is None:
             return _RopeAxes.apply(x, pos, pairs, theta, half, inverse)
+        _on(stream, x.get_device())
         with torch.cuda.stream(stream):         # the backward pass runs where the call did
             return _RopeAxes.apply(x, pos, pairs, theta, half, inverse)
     dev = x.get_device()

@@ -239,6 +239,10 @@ def test_rope_axes_gradient_streams_graphs_and_refusals():
     graph.replay()
     (want,) = torch.autograd.grad(op_rope_axes(x, pos, PAIRS[128]), x, g)
     assert torch.equal(out, want)
+    from types import SimpleNamespace
+    for v in (x, x.detach()):
+        with pytest.raises(ValueError, match="stream is on"):
+            op_rope_axes(v, pos, PAIRS[128], stream=SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0))
     for out in (torch.empty_like(x), x):
         with pytest.raises(ValueError, match="gradient"):
             op_rope_axes(x, pos, PAIRS[128], out=out)
