@@ -496,6 +496,40 @@ def test_attention_rows_of_no_sequence():
     assert (out[1:] == 3).all() and load() is not None
 
 
+@pytest.mark.parametrize("kv,nq,Hk,G,d,causal", [
+    ([1100], [300], 80, 1, 64, 1), ([2100], [130], 80, 4, 64, 0), ([1100], [300], 80, 1, 128, 100),
+    ([1200, 700, 1100], [300, 300, 40], 30, 1, 128, 1), ([1100, 1100, 1100], [300, 0, 300], 30, 1, 64, 1),
+    ([1030, 0, 1500], [290, 17, 5], 40, 1, 64, 0)])
+def test_attention_of_more_units_than_sms(kv, nq, Hk, G, d, causal):
+    """More than 148 units of 256 rows: the first round is whole, the rest in pieces, some of their units empty.  Rows of
+    no sequence are left alone, and pieces or not, an element is within both bounds."""
+    pairs = -(-max(nq) * G // 256)
+    units = pairs * Hk * len(kv)
+    assert units > 148 and units % 148 and max(kv) > 8 * 128
+    c = filled(29, len(kv), kv, Hk, 64, d)
+    cu = np.concatenate([[0], np.cumsum(nq)])
+    q = rand(34, cu[-1] + 3, Hk * G, d)
+    out = torch.full_like(q, 3.0)
+    check_attention(c, q, kv, cu, causal, out=out)
+    assert (out[cu[-1]:] == 3).all()
+    again, _ = attend(c, q, kv, cu, causal)
+    assert torch.equal(again[:cu[-1]], out[:cu[-1]])
+
+
+def test_workspace_does_not_grow_with_rows_of_no_sequence():
+    import ctypes
+    from streaming_causal_video_timestep_b200 import _lib, load
+    c = _lib.LaPagedCache(4096, 4096, 4096, 4096, 4096, 64, 2, 64, 64, 3, 64)
+    need = lambda tokens, heads, max_q, max_kv: load().la_op_attention_cache_fp8_workspace(  # noqa: E731
+        ctypes.byref(c), tokens, heads, max_q, max_kv)
+    assert need(1, 2, 1, 3000) == need(5000, 2, 1, 3000) > 0
+    assert need(300, 2, 300, 3000) == need(5000, 2, 300, 3000) > 0
+    assert need(3, 2, 5000, 3000) == need(3, 2, 3, 3000) > 0               # no sequence has more rows than there are
+    q = rand(35, 3, 2, 64)                                                  # and the call agrees: max_q above the rows
+    f = filled(36, 1, [3000], 2, 64, 64)
+    check_attention(f, q, [3000], [0, 3], 1, max_q=5000)
+
+
 @pytest.mark.parametrize("nq,G", [(1, 1), (1, 4), (40, 2)])
 def test_attention_peaked_and_far_apart(nq, G):
     """One key far above the rest, late (the running maximum moves) and early, and rows of q of very different sizes."""
