@@ -566,11 +566,12 @@ int la_op_attention_static(const void* q, int64_t Tq, int32_t H, int32_t d, int3
  *   pos DEVICE int32 [tokens, naxes]; pairs HOST int32 [naxes], sum n >= 1 and
  *   2 n <= head_dim; the first pairs[0] pairs turn with axis 0, the next
  *   pairs[1] with axis 1, and so on: pair j of an axis by
- *   a = pos * theta^(-j / pairs[axis]) (the stream's frequencies), theta >= 1.
+ *   a = pos * theta^(-j / pairs[axis]) (the stream's frequencies), theta in [1, 1e12].
  *   half 0: pair i of a row is elements (2i, 2i+1); 1: (i, i + n).
  *   out = (x0 cos a - x1 sin a, x0 sin a + x1 cos a), elements 2n.. unchanged;
  *   inverse != 0 turns by -a, which undoes the rotation and is its gradient.
- * Angles are exact modulo one turn for every int32 position.  x, out: DEVICE
+ * Angles are taken modulo one turn for every int32 position, |pos| * 2^-60 turns
+ * off at most.  x, out: DEVICE
  * [tokens, heads, head_dim] of dtype (LA_BF16, LA_FP16 or LA_FP32; fp32 inside,
  * rounded once), element strides of tokens and heads given, head_dim contiguous
  * and at most 256.  out == x with the same strides works in place; otherwise the
@@ -619,6 +620,10 @@ typedef struct la_paged_cache {
  *   become e4m3(code * old / new).  Rows of the page behind the last new token
  *   keep their codes.  A new value that is not finite makes the scale NaN (codes
  *   0), and it stays NaN until the page's first token is written again.
+ *   The rotation rounds sine, cosine, products and sums to fp32 one by one;
+ * la_op_rope_axes takes sine and cosine from a series and fuses products, within
+ * 5.2e-7 (|x0| + |x1|).  Keys that were rotated by it and are appended without
+ * positions may take another code where a value lies between two.
  * A page may receive tokens of one sequence only in a call, and a page that
  * several sequences read must not be appended to (copy it first): the library
  * does not check this.  A sequence whose cu_new, cache_len or block_table

@@ -64,7 +64,7 @@ template <int D> constexpr size_t rows_smem() {
 
 // HALVES: 8-row halves of the MMA's 16 rows that hold rows of this call; an empty half
 // costs its part of the softmax otherwise (at 1 row, 16 x 40 heads over up to 14040 keys:
-// 261 us, 270 with both).
+// 261 us, 273 with both).
 template <typename T, int D, int HALVES>
 __global__ void __launch_bounds__(WARPS * 32, 3)
 k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
@@ -340,7 +340,7 @@ k_attn_cache_rows(const __grid_constant__ AttnCacheParams p) {
 // `wpr` warps of a CTA share a row, each with its pieces' own maximum, and the first of
 // them joins what they found.  A lane holds 4 head dims; it reads the (maximum,
 // normaliser) of one piece of each 32, so the sums' loads wait for nothing (222 pieces
-// of 16 rows: 27 us with the pieces, 37 when a warp read them one after the other).
+// of 16 rows: 30 us with the pieces, 37 when a warp read them one after the other).
 constexpr int JOIN_WARPS = 8, JOIN_MAX_WARPS = 32;
 
 template <typename T, int D, bool FEW>

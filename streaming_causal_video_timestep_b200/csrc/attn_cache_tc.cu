@@ -19,17 +19,17 @@
 // tile waits for the loads that are under way for the next one (1.96 ms against
 // 1.57 ms at 4680 x 15600 x 40 x 128).
 //
-// Waits are bounded.  Lanes of a warp may see one end differently (each looks at the
-// clock and at the CTA's abort flag by itself), and what follows needs all of them, so
-// every answer is put to a vote.
-//
 // Scales: the score of a key is acc * ks * (row factor); log2(vs) enters the
 // exponent, so a page's P carries its value scale and the normaliser takes it out
 // again (sum * 1 / vs): scales cost no instruction an element beyond the scale and
 // offset that the exponent needs anyway.  A tile with a page whose value scale lies far
 // below an earlier one (see LA_CACHE_SPREAD) gets 0 for 1 / vs, and its weights are
-// summed by themselves, without the scales; the others pay 0 to 1.5 % for the question
-// (2 x 4680 q x 7800 keys x 16 heads, frame-causal: 594 us a call, 587 without).
+// summed by themselves, without the scales; the others pay 0 to 2 % for the question
+// (2 x 4680 q x 7800 keys x 16 heads, frame-causal: 600 us a call, 590 without).
+//
+// Waits are bounded.  Lanes of a warp may see one end differently (each looks at the
+// clock and at the CTA's abort flag by itself), and what follows needs all of them, so
+// every answer is put to a vote (602 us for the same case).
 #include <cstdio>
 
 #include "attn_cache.cuh"
@@ -507,8 +507,9 @@ k_attn_cache_tc(const __grid_constant__ AttnCacheParams p) {
           }
         }
         // At D = 64 the first half of P is handed over as soon as it is there: its products
-        // run beside the second half's exponentials (4 prompts of up to 1013 rows: 112.8
-        // us, 113.4 in one).  At D = 128 that was slower (1720 us at 4680 x 15600 x 40, 1575).
+        // run beside the second half's exponentials (4 prompts of up to 1013 rows: 113.9
+        // us, 114.9 in one).  At D = 128 that is no faster (4680 x 15600 x 40: 1611 us, 1589
+        // in one).
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           l += full ? softmax_exp<false>(s_base, 2 * h, valid, rowf, sc, m_ref)

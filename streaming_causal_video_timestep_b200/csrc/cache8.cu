@@ -10,9 +10,9 @@
 // reduction).  Bound: HBM.
 //
 // An element on the border between two codes goes to one or the other by the last bit of
-// its rotation, so that is the fp32 definition's to the bit: sine and cosine nearest to
-// the exact ones (in fp64, once for all the heads of a CTA), each product and sum
-// rounded by itself.
+// its rotation, so that is the fp32 definition's to the bit, as far as the angles are (off
+// by |pos| * 2^-60 turns at most): sine and cosine rounded to nearest (in fp64, once for
+// all the heads of a CTA), each product and sum rounded by itself.
 //
 // Scale: 2^k, the smallest with 448 * 2^k >= amax (k >= -64), read off amax's own
 // exponent and mantissa, so no rounding decides it.  A page that already holds

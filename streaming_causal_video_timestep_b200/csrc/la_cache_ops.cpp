@@ -27,7 +27,9 @@ bool known_dtype(int32_t dtype) { return dtype == LA_BF16 || dtype == LA_FP32 ||
 // omega_{a,j} = theta^(-j / pairs[a]), as a fraction of a turn in units of 2^-64: one
 // exp2l an axis and one multiplication a pair from the last power but at most 8 (long
 // double keeps the 64 bits that the product with a position uses; a call on one token
-// takes less time than 12 powl), off by at most 2^-59 relative after 8 * 8 + 8 factors.
+// takes less time than 12 powl).  With up to 15 + 7 factors and the cut to 2^-64 an entry
+// is off by 2^-60 turns at most: 2^-60.9 was the most for 1 to 128 pairs and 16 thetas
+// from 1 to 1e12, against powers with 113 bits.
 bool fill_table(RotaryTable& t, int32_t d, int32_t naxes, const int32_t* pairs, double theta, int32_t half,
                 int32_t inverse) {
   t.n = 0;
@@ -76,14 +78,14 @@ bool cache_fine(const la_paged_cache* c) {
 bool few_rows(int64_t max_q, int32_t heads, int32_t kv_heads) { return max_q * (heads / kv_heads) <= LA_CACHE_FEW_ROWS; }
 
 // How a call is laid out.  Few rows: enough CTAs for 3 on every SM with at least 128
-// keys each (one token over 1561 keys x 8 heads: 10.0 us; 11.0 with 256), and pieces of
+// keys each (one token over 1561 keys x 8 heads: 10.0 us; 11.2 with 256), and pieces of
 // about 2048 keys where that makes more, which evens out ragged lengths (16 x 40 heads
-// over up to 14040 keys: 261 us; 309 unsplit, 278 with 1024 keys).
+// over up to 14040 keys: 262 us; 311 unsplit, 279 with 1024 keys).
 // Many rows: one CTA an SM, 256 rows of a (sequence, key head) each.  The units behind
 // the last full round of the SMs are split along the keys, into the number of pieces that
 // makes the fewest key tiles in a row, a piece counted two tiles longer than it is for
-// its start and end and its part of the join (760 units of 122 tiles: 1735 us
-// unsplit, 1575 with the last 20 in 7 pieces each).
+// its start and end and its part of the join (760 units of 122 tiles: 1767 us
+// unsplit, 1589 with the last 20 in 7 pieces each).
 struct Plan {
   int nsplit = 1, pairs = 0, full = 0, units = 0;
   int64_t part_rows = 0;                           // of all pieces

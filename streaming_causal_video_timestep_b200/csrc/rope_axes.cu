@@ -116,8 +116,9 @@ cudaError_t launch(RopeAxesParams p, const RotaryTable& tab, int num_sms, cudaSt
   p.units = vec ? rot / N + (p.d - 2 * tab.n) / N : (p.d + 1) / 2;
   const long long per_head = p.tokens * p.units;
   // One head a thread until the grid has 1024 threads for every SM, then up to 8: the
-  // sines are shared and more loads are under way (4680 x 40 x 128 bf16: 14.8 us, 17.3
-  // with 4096; 3601 x 24 x 64 fp32 halves: 7.6, 9.2 with 2048, 14.3 with 4096).
+  // sines are shared and more loads are under way (every output in memory of its own, 4680
+  // x 40 x 128 bf16: 18.1 us, 18.2 with 4096; 3601 x 24 x 64 fp32 halves: 9.9, 11.4 with
+  // 2048, 15.9 with 4096).
   const long long hpt = per_head * p.heads / (num_sms * 1024LL);
   p.heads_per_thread = static_cast<int>(hpt < 1 ? 1 : (hpt > 8 ? 8 : hpt));
   const long long gx = (per_head + 255) / 256;

@@ -1,10 +1,10 @@
 // Rotary positions with several axes, shared by k_rope_axes and the cache append.
 //
 // Pair j (of n) turns by pos[axis(j)] * omega_j.  The angle is kept in turns as a
-// 64-bit fixed-point fraction: omega_j / (2 pi) * 2^64 is rounded once on the host
-// and the product with the (signed) position wraps modulo 2^64, which is exactly
-// "modulo one turn".  Its error is |pos| * 2^-61 turns at most, for every position an
-// int32 holds, where pos * omega in fp32 would lose 2^-24 * pos * omega radians (6e-3
+// 64-bit fixed-point fraction: omega_j / (2 pi) * 2^64 comes from the host, 2^-60 turns
+// off at most, and the product with the (signed) position wraps modulo 2^64, which is
+// exactly "modulo one turn".  Its error is |pos| * 2^-60 turns at most, for every position
+// an int32 holds, where pos * omega in fp32 would lose 2^-24 * pos * omega radians (6e-3
 // at position 1e5).  Its top 32 bits, as an integer, give the quadrant and the signed
 // rest within an eighth of a turn exactly; the rest goes to fp32 once and into the
 // Taylor series of sine and cosine about 0 (next terms at pi/4: 3e-9 and 4e-10).
@@ -55,7 +55,8 @@ struct PairTable {
     const float2 v = turn_cos_sin(static_cast<uint32_t>(ph >> 32));
     return make_float2(v.x, inverse ? -v.y : v.y);
   }
-  // The same, each the fp32 value nearest to the exact one (computed in fp64).
+  // The same, each the fp32 value nearest to that of the table's angle (computed in fp64),
+  // and so of the exact one but where |pos| * 2^-60 turns decide.
   __device__ __forceinline__ float2 cos_sin_nearest(int j, const int* pos) const {
     const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(pos[axis[j]])) * turn[j];
     double s, c;
